@@ -8,6 +8,13 @@ no CPU fallback: if the library is missing the import of an op fails loudly.
     o, state_out = prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None)
     o = decode(q, k, v, g, beta, state)          # state updated in place
 
+    o, state_out = linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None)   # without the delta term
+    o = linear_decode(q, k, v, g, state)
+
+    codes, exps = state_pool(n_slots, Hv, dv, dk)  # states of many sequences, in 8 bits
+    state_store(state, codes, exps, slots)
+    state = state_load(codes, exps, slots)
+
 q, k and v may be bf16, f16 or fp32 (all three the same); g, beta and the
 prefill states are fp32.
 """
@@ -21,6 +28,8 @@ import torch
 
 __all__ = ["prefill", "prefill_noalloc", "decode", "prefill_workspace_bytes", "prefill_plan", "device_error",
            "wait_selftest",
+           "linear_prefill", "linear_prefill_workspace_bytes", "linear_decode",
+           "state_pool", "state_store", "state_load",
            "GdnError",
            "lib", "debug_lib", "library_path", "debug_library_path", "GDN_BF16", "GDN_F32", "GDN_F16"]
 
@@ -77,6 +86,13 @@ SIGNATURES = {
                             _vp, _fp, _vp, _sz, _vp, _vp]),
     "gdn_prefill_plan": (_i, [_i, _i64, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "gdn_debug_checks": (_i, []),
+    "gdn_linear_prefill_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i]),
+    "gdn_linear_prefill": (_i, [_vp, _vp, _vp, _fp, _i, _fp, _i32p, _i, _i64, _i, _i, _i, _i, _f, _i,
+                                _vp, _fp, _vp, _sz, _vp]),
+    "gdn_linear_decode": (_i, [_vp, _vp, _vp, _fp, _i, _fp, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
+    "gdn_linear_decode_bf16_state": (_i, [_vp, _vp, _vp, _fp, _i, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
+    "gdn_state_store": (_i, [_vp, _i, _i32p, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "gdn_state_load": (_i, [_vp, _vp, _i32p, _i, _i, _i, _i, _i, _i, _vp, _i, _vp]),
 }
 
 
@@ -265,3 +281,157 @@ def wait_selftest(max_wait_us: int = 2000, stream=None) -> None:
 def device_error(stream=None) -> None:
     """Synchronise and raise GdnError if a bounded device wait ran out."""
     _check(lib().gdn_device_error(_stream_handle(stream)))
+
+
+# ------------------------------------------------------- linear attention ---
+def _on(device, **tensors):
+    """The tensors (None: left out) are all on `device`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, is on {t.device}")
+
+
+def _stream_of(device, stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _decay(g, rows, Hv):
+    """The token stride of log-decays [rows, Hv] or [Hv]."""
+    _dev(g, "g", torch.float32)
+    if tuple(g.shape) == (Hv,):
+        return 0
+    _shape(g, "g", (rows, Hv))
+    return Hv
+
+
+def linear_prefill_workspace_bytes(n_seqs, total_T, Hv, dk, dv, dtype=torch.bfloat16) -> int:
+    return int(lib().gdn_linear_prefill_workspace_bytes(n_seqs, total_T, Hv, dk, dv, _torch_dtype_code(dtype)))
+
+
+def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=None, state_out=None,
+                   workspace=None, stream=None):
+    """Decayed linear attention over packed sequences: S_t = exp(g_t) S_{t-1} +
+    v_t k_t^T, o_t = scale S_t q_t (scale None: dk^-1/2).
+
+    q, k [T, Hqk, dk]; v [T, Hv, dv] (bf16, f16 or fp32, same dtype); g fp32
+    [T, Hv], or [Hv] for a decay fixed per value head; state_in [N, Hv, dv, dk]
+    fp32 or None; cu_seqlens [N+1] int32 (None = one sequence of T tokens).
+    state_out may be state_in. Returns (o [T, Hv, dv], state_out [N, Hv, dv, dk]).
+    """
+    _dev(q, "q"); _dev(k, "k", q.dtype); _dev(v, "v", q.dtype)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k must be [T, Hqk, dk] and v [T, Hv, dv]")
+    dtype = _dtype_code(q)
+    T, Hqk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    _shape(k, "k", (T, Hqk, dk)); _shape(v, "v", (T, Hv, dv))
+    g_stride = _decay(g, T, Hv)
+    with torch.cuda.device(q.device):
+        if cu_seqlens is None:
+            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=q.device)
+        _dev(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError(f"cu_seqlens must have shape (N + 1,), got {tuple(cu_seqlens.shape)}")
+        N = cu_seqlens.numel() - 1
+        if state_in is not None:
+            _dev(state_in, "state_in", torch.float32); _shape(state_in, "state_in", (N, Hv, dv, dk))
+        if o is None:
+            o = torch.empty(T, Hv, dv, dtype=q.dtype, device=q.device)
+        _dev(o, "o", q.dtype); _shape(o, "o", (T, Hv, dv))
+        if state_out is None:
+            state_out = torch.empty(N, Hv, dv, dk, dtype=torch.float32, device=q.device)
+        _dev(state_out, "state_out", torch.float32); _shape(state_out, "state_out", (N, Hv, dv, dk))
+        need = linear_prefill_workspace_bytes(N, T, Hv, dk, dv, q.dtype)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if workspace is not None:
+            _dev(workspace, "workspace")
+        _on(q.device, k=k, v=v, g=g, state_in=state_in, cu_seqlens=cu_seqlens, o=o, state_out=state_out,
+            workspace=workspace)
+        _check(lib().gdn_linear_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride,
+            state_in.data_ptr() if state_in is not None else None, cu_seqlens.data_ptr(),
+            N, T, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), state_out.data_ptr(),
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+            _stream_of(q.device, stream)))
+    return o, state_out
+
+
+def linear_decode(q, k, v, g, state, *, scale=None, o=None, stream=None):
+    """One step of decayed linear attention: q, k [B, Hqk, dk]; v [B, Hv, dv]; g
+    [B, Hv] or [Hv]; state [B, Hv, dv, dk] updated in place -- fp32
+    (gdn_linear_decode) or bf16 (gdn_linear_decode_bf16_state). Returns o [B, Hv, dv]."""
+    _dev(q, "q"); _dev(k, "k", q.dtype); _dev(v, "v", q.dtype); _dev(state, "state")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k must be [B, Hqk, dk] and v [B, Hv, dv]")
+    dtype = _dtype_code(q)
+    if state.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"state must be fp32 or bf16, got {state.dtype}")
+    B, Hqk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    _shape(k, "k", (B, Hqk, dk)); _shape(v, "v", (B, Hv, dv)); _shape(state, "state", (B, Hv, dv, dk))
+    g_stride = _decay(g, B, Hv)
+    with torch.cuda.device(q.device):
+        if o is None:
+            o = torch.empty(B, Hv, dv, dtype=q.dtype, device=q.device)
+        _dev(o, "o", q.dtype); _shape(o, "o", (B, Hv, dv))
+        _on(q.device, k=k, v=v, g=g, state=state, o=o)
+        fn = lib().gdn_linear_decode if state.dtype == torch.float32 else lib().gdn_linear_decode_bf16_state
+        _check(fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride, state.data_ptr(),
+                  B, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), _stream_of(q.device, stream)))
+    return o
+
+
+# ------------------------------------------------------------- state pool ---
+_CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+def state_pool(n_slots, Hv, dv, dk, *, dtype=torch.float8_e4m3fn, device="cuda"):
+    """(codes [n_slots, Hv, dv, dk], exps [n_slots, Hv, dv, dk / min(32, dk)]) of
+    zero states: a pool for state_store and state_load, in float8_e4m3fn or int8."""
+    if dtype not in _CODES:
+        raise TypeError(f"codes must be float8_e4m3fn or int8, got {dtype}")
+    codes = torch.zeros(n_slots, Hv, dv, dk, dtype=torch.int8, device=device).view(dtype)
+    return codes, torch.zeros(n_slots, Hv, dv, dk // min(32, dk), dtype=torch.uint8, device=device)
+
+
+def _pool_args(codes, exps, slots, state):
+    _dev(codes, "codes"); _dev(exps, "exps", torch.uint8); _dev(slots, "slots", torch.int32); _dev(state, "state")
+    if codes.dtype not in _CODES:
+        raise TypeError(f"codes must be float8_e4m3fn or int8, got {codes.dtype}")
+    if codes.dim() != 4 or slots.dim() != 1:
+        raise ValueError("codes must be [n_slots, Hv, dv, dk] and slots [n]")
+    if state.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"state must be fp32 or bf16, got {state.dtype}")
+    n_slots, Hv, dv, dk = codes.shape
+    n = slots.numel()
+    _shape(exps, "exps", (n_slots, Hv, dv, dk // min(32, dk) if dk else 0))
+    _shape(state, "state", (n, Hv, dv, dk))
+    _on(codes.device, exps=exps, slots=slots, state=state)
+    return n, n_slots, Hv, dk, dv, _CODES[codes.dtype], GDN_F32 if state.dtype == torch.float32 else GDN_BF16
+
+
+def state_store(state, codes, exps, slots, *, stream=None) -> None:
+    """Quantises state [n, Hv, dv, dk] (fp32 or bf16) into the slots [n] int32 of
+    the pool: value = code 2^(exp - 127), one exponent byte for each 32 values
+    along dk. A slot outside the pool is passed over; of several states for one
+    slot the last is kept."""
+    n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
+    with torch.cuda.device(codes.device):
+        _check(lib().gdn_state_store(state.data_ptr(), sdt, slots.data_ptr(), n, n_slots, Hv, dk, dv, code,
+                                     codes.data_ptr(), exps.data_ptr(), _stream_of(codes.device, stream)))
+
+
+def state_load(codes, exps, slots, *, state=None, dtype=torch.float32, stream=None):
+    """Reads slots [n] int32 of the pool into state [n, Hv, dv, dk] (fp32 or bf16;
+    allocated as `dtype` if not given) and returns it. A slot outside the pool
+    gives a zero state."""
+    _dev(codes, "codes"); _dev(slots, "slots", torch.int32)
+    if state is None:
+        state = torch.empty(slots.numel(), *codes.shape[1:], dtype=dtype, device=codes.device)
+    n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
+    with torch.cuda.device(codes.device):
+        _check(lib().gdn_state_load(codes.data_ptr(), exps.data_ptr(), slots.data_ptr(), n, n_slots, Hv, dk, dv,
+                                    code, state.data_ptr(), sdt, _stream_of(codes.device, stream)))
+    return state

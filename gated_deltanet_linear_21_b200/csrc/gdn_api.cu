@@ -8,6 +8,7 @@
 #include <set>
 #include <string>
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 
 #include "gdn.h"
@@ -15,6 +16,8 @@
 #include "decode.cuh"
 #include "prefill_simt.cuh"
 #include "prefill_pc.cuh"
+#include "linear.cuh"
+#include "state_pool.cuh"
 
 #include <cudaTypedefs.h>
 
@@ -347,11 +350,191 @@ gdn_status launch_prefill_pc(const void* q, const void* k, const void* v, const 
   return launch_pc<128, __nv_bfloat16>(qm, km, vm, om, prm, sms, st);
 }
 
+// ------------------------------------------------------ linear attention ---
+// Calls f with a null pointer of the C++ type of dtype.
+template <typename F>
+gdn_status with_dtype(gdn_dtype dtype, F f) {
+  if (dtype == GDN_F32) return f(static_cast<float*>(nullptr));
+  if (dtype == GDN_F16) return f(static_cast<__half*>(nullptr));
+  return f(static_cast<__nv_bfloat16*>(nullptr));
+}
+// Calls f with dk as a compile-time constant.
+template <typename F>
+gdn_status with_dk(int dk, F f) {
+  switch (dk) {
+    case 16: return f(std::integral_constant<int, 16>());
+    case 32: return f(std::integral_constant<int, 32>());
+    case 64: return f(std::integral_constant<int, 64>());
+    default: return f(std::integral_constant<int, 128>());
+  }
+}
+
+template <typename TS>
+gdn_status linear_decode(const char* fn, const void* q, const void* k, const void* v, const float* g, int g_stride,
+                         TS* state, int B, int Hqk, int Hv, int dk, int dv, float scale, gdn_dtype dtype, void* o,
+                         void* stream) {
+  bool done = false;
+  // (g stands in for the beta of the shared checks)
+  if (gdn_status s = check_decode(fn, q, k, v, g, g, state, B, Hqk, Hv, dk, dv, dtype, o, &done)) return s;
+  if (g_stride != 0 && g_stride != Hv)
+    return fail(GDN_ERR_INVALID_ARG, "%s: g_stride=%d (0 or Hv=%d)", fn, g_stride, Hv);
+  if (done) return ok();
+  if (scale <= 0.f) scale = 1.0f / sqrtf((float)dk);
+  return with_dtype(dtype, [&](auto* tag) {
+    using T = std::remove_pointer_t<decltype(tag)>;
+    return with_dk(dk, [&](auto dkc) {
+      constexpr int DK = decltype(dkc)::value;
+      using Sh = gdn::DecodeShape<DK, TS>;
+      const dim3 grid((unsigned)(B * Hv), (unsigned)((dv + Sh::kRowsPerCta - 1) / Sh::kRowsPerCta));
+      gdn::lin::decode_kernel<T, DK, TS><<<grid, Sh::kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+          static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_stride, state, Hqk, Hv,
+          dv, scale, static_cast<T*>(o));
+      return launch_status(fn);
+    });
+  });
+}
+
+// ------------------------------------------------------------ state pool ---
+gdn_status check_pool(const char* fn, const void* state, gdn_dtype state_dtype, const int32_t* slots, int n,
+                      int n_slots, int Hv, int dk, int dv, gdn_code code, const void* codes, const uint8_t* exps,
+                      bool* done) {
+  *done = false;
+  if (n < 0 || n_slots < 0) return fail(GDN_ERR_INVALID_ARG, "%s: n=%d, n_slots=%d", fn, n, n_slots);
+  if (Hv <= 0) return fail(GDN_ERR_INVALID_ARG, "%s: Hv=%d", fn, Hv);
+  if (!head_dim_ok(dk) || !head_dim_ok(dv))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: dk=%d, dv=%d (supported: 16, 32, 64, 128)", fn, dk, dv);
+  if (state_dtype != GDN_F32 && state_dtype != GDN_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "%s: state type %d (GDN_F32 or GDN_BF16)", fn, (int)state_dtype);
+  if (code != GDN_CODE_E4M3 && code != GDN_CODE_I8) return fail(GDN_ERR_INVALID_ARG, "%s: unknown code %d", fn, (int)code);
+  const int64_t tiles = ((int64_t)Hv * dv * dk + gdn::pool::kTile - 1) / gdn::pool::kTile;
+  if (n > 0 && tiles > 0x7fffffff / n) return fail(GDN_ERR_INVALID_ARG, "%s: n*Hv too large", fn);
+  if (n == 0) {
+    *done = true;
+    return ok();
+  }
+  if (!state || !slots || (n_slots > 0 && (!codes || !exps)))
+    return fail(GDN_ERR_INVALID_ARG, "%s: pointers must not be NULL", fn);
+  if (!aligned16(state) || !aligned16(codes))
+    return fail(GDN_ERR_INVALID_ARG, "%s: state and codes must be 16-byte aligned", fn);
+  if (!aligned4(slots)) return fail(GDN_ERR_INVALID_ARG, "%s: slots must be 4-byte aligned", fn);
+  return GDN_OK;
+}
+
+template <typename F>
+gdn_status with_pool_types(gdn_code code, gdn_dtype state_dtype, int dk, F f) {
+  auto group = [&](auto c, auto* s) {
+    return dk == 16 ? f(c, s, std::integral_constant<int, 4>()) : f(c, s, std::integral_constant<int, 8>());
+  };
+  auto st = [&](auto c) {
+    return state_dtype == GDN_F32 ? group(c, static_cast<float*>(nullptr))
+                                  : group(c, static_cast<__nv_bfloat16*>(nullptr));
+  };
+  return code == GDN_CODE_E4M3 ? st(gdn::pool::E4M3()) : st(gdn::pool::I8());
+}
+
 }  // namespace
 
 extern "C" {
 
-int gdn_version(void) { return (0 << 16) | 4; }
+size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype) {
+  (void)n_seqs; (void)total_T; (void)Hv; (void)dk; (void)dv; (void)dtype;
+  return 0;
+}
+
+gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const float* g, int g_stride,
+                              const float* state_in, const int32_t* cu_seqlens, int n_seqs, int64_t total_T, int Hqk,
+                              int Hv, int dk, int dv, float scale, gdn_dtype dtype, void* o, float* state_out,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "gdn_linear_prefill";
+  if (n_seqs < 0) return fail(GDN_ERR_INVALID_ARG, "%s: n_seqs=%d < 0", fn, n_seqs);
+  if (total_T < 0 || total_T >= (int64_t(1) << 31))
+    return fail(GDN_ERR_INVALID_ARG, "%s: total_T=%lld out of range", fn, (long long)total_T);
+  if (Hqk <= 0 || Hv <= 0 || Hv % Hqk != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: Hv=%d must be a positive multiple of Hqk=%d", fn, Hv, Hqk);
+  if (!head_dim_ok(dk) || !head_dim_ok(dv))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: dk=%d, dv=%d (supported: 16, 32, 64, 128)", fn, dk, dv);
+  if (!dtype_ok(dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+  if (g_stride != 0 && g_stride != Hv)
+    return fail(GDN_ERR_INVALID_ARG, "%s: g_stride=%d (0 or Hv=%d)", fn, g_stride, Hv);
+  if (n_seqs > 65535 || Hv > 65535)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: n_seqs=%d, Hv=%d (at most 65535 each)", fn, n_seqs, Hv);
+  if (n_seqs == 0) return ok();
+  if (!cu_seqlens || !state_out)
+    return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens and state_out must not be NULL", fn);
+  if (total_T > 0 && (!q || !k || !v || !g || !o))
+    return fail(GDN_ERR_INVALID_ARG, "%s: q, k, v, g and o must not be NULL", fn);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state_out) || !aligned16(state_in))
+    return fail(GDN_ERR_INVALID_ARG, "%s: q, k, v, o and the states must be 16-byte aligned", fn);
+  if (!aligned4(g) || !aligned4(cu_seqlens))
+    return fail(GDN_ERR_INVALID_ARG, "%s: g and cu_seqlens must be 4-byte aligned", fn);
+  const size_t need = gdn_linear_prefill_workspace_bytes(n_seqs, total_T, Hv, dk, dv, dtype);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace needs %zu bytes (16-byte aligned), got %zu", fn, need,
+                workspace_bytes);
+  if (scale <= 0.f) scale = 1.0f / sqrtf((float)dk);
+  return with_dtype(dtype, [&](auto* tag) {
+    using T = std::remove_pointer_t<decltype(tag)>;
+    return with_dk(dk, [&](auto dkc) {
+      const dim3 grid((unsigned)((dv + gdn::lin::kScanRows - 1) / gdn::lin::kScanRows), (unsigned)Hv, (unsigned)n_seqs);
+      gdn::lin::scan_kernel<T, decltype(dkc)::value>
+          <<<grid, gdn::lin::kScanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+              static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_stride, state_in,
+              cu_seqlens, Hqk, Hv, dv, scale, static_cast<T*>(o), state_out, (long long)total_T);
+      return launch_status(fn);
+    });
+  });
+}
+
+gdn_status gdn_linear_decode(const void* q, const void* k, const void* v, const float* g, int g_stride, float* state,
+                             int B, int Hqk, int Hv, int dk, int dv, float scale, gdn_dtype dtype, void* o,
+                             void* stream) {
+  return linear_decode("gdn_linear_decode", q, k, v, g, g_stride, state, B, Hqk, Hv, dk, dv, scale, dtype, o, stream);
+}
+
+gdn_status gdn_linear_decode_bf16_state(const void* q, const void* k, const void* v, const float* g, int g_stride,
+                                        void* state, int B, int Hqk, int Hv, int dk, int dv, float scale,
+                                        gdn_dtype dtype, void* o, void* stream) {
+  return linear_decode("gdn_linear_decode_bf16_state", q, k, v, g, g_stride, static_cast<__nv_bfloat16*>(state), B,
+                       Hqk, Hv, dk, dv, scale, dtype, o, stream);
+}
+
+gdn_status gdn_state_store(const void* state, gdn_dtype state_dtype, const int32_t* slots, int n, int n_slots, int Hv,
+                           int dk, int dv, gdn_code code, void* codes, uint8_t* exps, void* stream) {
+  bool done = false;
+  if (gdn_status s = check_pool("gdn_state_store", state, state_dtype, slots, n, n_slots, Hv, dk, dv, code, codes,
+                                exps, &done))
+    return s;
+  if (done) return ok();
+  const long long per_state = (long long)Hv * dv * dk;
+  const int tiles = (int)((per_state + gdn::pool::kTile - 1) / gdn::pool::kTile);
+  return with_pool_types(code, state_dtype, dk, [&](auto c, auto* tag, auto grp) {
+    using TS = std::remove_pointer_t<decltype(tag)>;
+    gdn::pool::store_kernel<decltype(c), TS, decltype(grp)::value>
+        <<<(unsigned)n * tiles, gdn::pool::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+            static_cast<const TS*>(state), slots, n, n_slots, tiles, per_state, static_cast<uint32_t*>(codes), exps);
+    return launch_status("gdn_state_store");
+  });
+}
+
+gdn_status gdn_state_load(const void* codes, const uint8_t* exps, const int32_t* slots, int n, int n_slots, int Hv,
+                          int dk, int dv, gdn_code code, void* state, gdn_dtype state_dtype, void* stream) {
+  bool done = false;
+  if (gdn_status s = check_pool("gdn_state_load", state, state_dtype, slots, n, n_slots, Hv, dk, dv, code, codes, exps,
+                                &done))
+    return s;
+  if (done) return ok();
+  const long long per_state = (long long)Hv * dv * dk;
+  const int tiles = (int)((per_state + gdn::pool::kTile - 1) / gdn::pool::kTile);
+  return with_pool_types(code, state_dtype, dk, [&](auto c, auto* tag, auto grp) {
+    using TS = std::remove_pointer_t<decltype(tag)>;
+    gdn::pool::load_kernel<decltype(c), TS, decltype(grp)::value>
+        <<<(unsigned)n * tiles, gdn::pool::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+            static_cast<const uint32_t*>(codes), exps, slots, n_slots, tiles, per_state, static_cast<TS*>(state));
+    return launch_status("gdn_state_load");
+  });
+}
+
+int gdn_version(void) { return (0 << 16) | 5; }
 
 const char* gdn_last_error(void) { return t_last_error.c_str(); }
 

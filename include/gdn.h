@@ -267,6 +267,91 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
                                  int B, int Hqk, int Hv, int dk, int dv,
                                  float scale, gdn_dtype dtype, void *o, void *stream);
 
+/*
+ * Decayed linear attention: the recurrence without the delta term, for the
+ * layers of hybrid models that carry the same kind of state,
+ *
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,     o_t = scale S_t q_t
+ *
+ * over packed prompts. q and k are used as given (not normalised). Not on the
+ * Herbert pages, whose recurrent layers are gated delta rule ones; it is the
+ * same family's simpler member.
+ *
+ *   q, k       [total_T, Hqk, dk]    dtype
+ *   v          [total_T, Hv, dv]     dtype
+ *   g          fp32 log-decay (<= 0 in normal use): [total_T, Hv] with
+ *              g_stride = Hv (one for each token and value head), or [Hv] with
+ *              g_stride = 0 (one fixed for each value head). -infinity is a
+ *              reset: the state before that token counts for nothing from it on.
+ *   state_in   [n_seqs, Hv, dv, dk]  fp32, or NULL for zero states
+ *   cu_seqlens [n_seqs + 1] int32, as gdn_prefill's
+ *   o          [total_T, Hv, dv]     dtype (output); rows before the first
+ *              sequence and behind the last are left as they were
+ *   state_out  [n_seqs, Hv, dv, dk]  fp32 (output); may be state_in. A sequence
+ *              of no tokens gets its state_in.
+ *   workspace  gdn_linear_prefill_workspace_bytes() bytes, 16-byte aligned (its
+ *              contents on entry do not matter). Calls that may overlap on the
+ *              GPU, captured graphs among them, need workspaces of their own.
+ *
+ * Supported: every dtype, dk and dv in {16, 32, 64, 128}; n_seqs and Hv up to
+ * 65535. State and sums are fp32.
+ */
+size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype);
+gdn_status gdn_linear_prefill(const void *q, const void *k, const void *v,
+                              const float *g, int g_stride,
+                              const float *state_in, const int32_t *cu_seqlens,
+                              int n_seqs, int64_t total_T, int Hqk, int Hv, int dk, int dv,
+                              float scale, gdn_dtype dtype,
+                              void *o, float *state_out,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One step of decayed linear attention for B sequences: as gdn_decode, without
+ * beta and the normalisation. g is [B, Hv] with g_stride = Hv or [Hv] with
+ * g_stride = 0. The state [B, Hv, dv, dk] is updated in place, in fp32, or in
+ * bf16 (gdn_linear_decode_bf16_state: fp32 arithmetic, written back rounded to
+ * nearest even; o is computed from the state before it is rounded).
+ */
+gdn_status gdn_linear_decode(const void *q, const void *k, const void *v,
+                             const float *g, int g_stride, float *state,
+                             int B, int Hqk, int Hv, int dk, int dv,
+                             float scale, gdn_dtype dtype, void *o, void *stream);
+gdn_status gdn_linear_decode_bf16_state(const void *q, const void *k, const void *v,
+                                        const float *g, int g_stride, void *state,
+                                        int B, int Hqk, int Hv, int dk, int dv,
+                                        float scale, gdn_dtype dtype, void *o, void *stream);
+
+/*
+ * A pool of recurrent states (gated delta rule's or linear attention's) in 8
+ * bits, for sequences that are set aside and for cached prefixes.
+ *
+ *   codes  [n_slots, Hv, dv, dk]  8-bit codes
+ *   exps   [n_slots, Hv, dv, dk / 32] (dk / 16 where dk = 16)  exponent bytes
+ *
+ * A value is code * 2^(exp - 127). Each group of 32 values along dk (16 where
+ * dk = 16) has the smallest exponent byte (0 at least) with which its largest
+ * magnitude fits the codes, 448 for GDN_CODE_E4M3 and 127 for GDN_CODE_I8;
+ * codes are rounded to nearest even. Scaling by powers of two is exact, so a
+ * state that is loaded and stored again keeps its values. A group that holds
+ * an infinity or a NaN gets exponent byte 255 and loads as NaN. Zeroed codes
+ * and exps are zero states.
+ *
+ * gdn_state_store writes state i of `state` [n, Hv, dv, dk] (GDN_F32 or
+ * GDN_BF16) into slot slots[i]; a slot outside [0, n_slots) stands for a state
+ * that is not kept, and of several states for one slot the last is kept.
+ * gdn_state_load reads slot slots[i] into state i; a slot outside [0, n_slots)
+ * stands for a sequence without a past and gives zeros. slots is read on the
+ * device. state must not overlap codes and exps.
+ */
+typedef enum gdn_code {
+    GDN_CODE_E4M3 = 0,   /* 4 exponent bits, 3 mantissa bits, no infinities */
+    GDN_CODE_I8 = 1      /* integers -127 .. 127 */
+} gdn_code;
+gdn_status gdn_state_store(const void *state, gdn_dtype state_dtype, const int32_t *slots, int n, int n_slots,
+                           int Hv, int dk, int dv, gdn_code code, void *codes, uint8_t *exps, void *stream);
+gdn_status gdn_state_load(const void *codes, const uint8_t *exps, const int32_t *slots, int n, int n_slots,
+                          int Hv, int dk, int dv, gdn_code code, void *state, gdn_dtype state_dtype, void *stream);
+
 /* Message describing the calling thread's most recent failure ("" if none). */
 const char *gdn_last_error(void);
 
