@@ -20,6 +20,7 @@ prefill states are fp32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -291,8 +292,18 @@ def _on(device, **tensors):
             raise ValueError(f"{name} must be on {device}, is on {t.device}")
 
 
-def _stream_of(device, stream) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+_here = contextlib.nullcontext()
+
+
+def _running_on(device, stream):
+    """A context in which `device` and `stream` (None: the device's current one) are
+    current: what a call allocates belongs to the stream that its kernels run on, so
+    the memory is not handed out again before they have run."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _decay(g, rows, Hv):
@@ -326,7 +337,7 @@ def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=
     Hv, dv = v.shape[1], v.shape[2]
     _shape(k, "k", (T, Hqk, dk)); _shape(v, "v", (T, Hv, dv))
     g_stride = _decay(g, T, Hv)
-    with torch.cuda.device(q.device):
+    with _running_on(q.device, stream):
         if cu_seqlens is None:
             cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=q.device)
         _dev(cu_seqlens, "cu_seqlens", torch.int32)
@@ -354,7 +365,7 @@ def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=
             N, T, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), state_out.data_ptr(),
             workspace.data_ptr() if workspace is not None else None,
             workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _stream_of(q.device, stream)))
+            torch.cuda.current_stream().cuda_stream))
     return o, state_out
 
 
@@ -372,14 +383,14 @@ def linear_decode(q, k, v, g, state, *, scale=None, o=None, stream=None):
     Hv, dv = v.shape[1], v.shape[2]
     _shape(k, "k", (B, Hqk, dk)); _shape(v, "v", (B, Hv, dv)); _shape(state, "state", (B, Hv, dv, dk))
     g_stride = _decay(g, B, Hv)
-    with torch.cuda.device(q.device):
+    with _running_on(q.device, stream):
         if o is None:
             o = torch.empty(B, Hv, dv, dtype=q.dtype, device=q.device)
         _dev(o, "o", q.dtype); _shape(o, "o", (B, Hv, dv))
         _on(q.device, k=k, v=v, g=g, state=state, o=o)
         fn = lib().gdn_linear_decode if state.dtype == torch.float32 else lib().gdn_linear_decode_bf16_state
         _check(fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride, state.data_ptr(),
-                  B, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), _stream_of(q.device, stream)))
+                  B, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), torch.cuda.current_stream().cuda_stream))
     return o
 
 
@@ -418,9 +429,9 @@ def state_store(state, codes, exps, slots, *, stream=None) -> None:
     along dk. A slot outside the pool is passed over; of several states for one
     slot the last is kept."""
     n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
-    with torch.cuda.device(codes.device):
+    with _running_on(codes.device, stream):
         _check(lib().gdn_state_store(state.data_ptr(), sdt, slots.data_ptr(), n, n_slots, Hv, dk, dv, code,
-                                     codes.data_ptr(), exps.data_ptr(), _stream_of(codes.device, stream)))
+                                     codes.data_ptr(), exps.data_ptr(), torch.cuda.current_stream().cuda_stream))
 
 
 def state_load(codes, exps, slots, *, state=None, dtype=torch.float32, stream=None):
@@ -428,10 +439,10 @@ def state_load(codes, exps, slots, *, state=None, dtype=torch.float32, stream=No
     allocated as `dtype` if not given) and returns it. A slot outside the pool
     gives a zero state."""
     _dev(codes, "codes"); _dev(slots, "slots", torch.int32)
-    if state is None:
-        state = torch.empty(slots.numel(), *codes.shape[1:], dtype=dtype, device=codes.device)
-    n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
-    with torch.cuda.device(codes.device):
+    with _running_on(codes.device, stream):
+        if state is None:
+            state = torch.empty(slots.numel(), *codes.shape[1:], dtype=dtype, device=codes.device)
+        n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
         _check(lib().gdn_state_load(codes.data_ptr(), exps.data_ptr(), slots.data_ptr(), n, n_slots, Hv, dk, dv,
-                                    code, state.data_ptr(), sdt, _stream_of(codes.device, stream)))
+                                    code, state.data_ptr(), sdt, torch.cuda.current_stream().cuda_stream))
     return state

@@ -17,6 +17,7 @@
 #include "prefill_simt.cuh"
 #include "prefill_pc.cuh"
 #include "linear.cuh"
+#include "linear_tc.cuh"
 #include "state_pool.cuh"
 
 #include <cudaTypedefs.h>
@@ -168,13 +169,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // 3-D map of 16-bit elements (bf16 or f16) over a token-major [T][H][D] tensor:
-// dims (D, H, T), box (box_d, 1, 64).
-bool make_map(CUtensorMap* m, const void* base, int D, int H, int T, int box_d, CUtensorMapDataType type) {
+// dims (D, H, T), box (box_d, 1, box_t).
+bool make_map(CUtensorMap* m, const void* base, int D, int H, int T, int box_d, CUtensorMapDataType type,
+              int box_t = gdn::pc::kC) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
-  cuuint32_t box[3] = {(cuuint32_t)box_d, 1, (cuuint32_t)gdn::pc::kC};
+  cuuint32_t box[3] = {(cuuint32_t)box_d, 1, (cuuint32_t)box_t};
   cuuint32_t estr[3] = {1, 1, 1};
   const int row_bytes = box_d * 2;
   CUtensorMapSwizzle sw = row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
@@ -369,6 +371,72 @@ gdn_status with_dk(int dk, F f) {
   }
 }
 
+// 3-D map over fp32 states [rows][dv][dk]: boxes of 32 columns and 128 rows of one state.
+bool make_state_map(CUtensorMap* m, const void* base, int dk, int dv, int64_t rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)dk, (cuuint64_t)dv, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)dk * 4, (cuuint64_t)dv * dk * 4};
+  cuuint32_t box[3] = {32, 128, 1}, estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kLinearCtas = 148;   // CTAs that the workspace is laid out for: one on each SM
+
+bool linear_on_tensor_cores(gdn_dtype dtype, int64_t total_T) { return dtype != GDN_F32 && total_T > 0; }
+
+// Blocks of 128 tokens per segment. Fewer make more items, so that one sequence's
+// heads fill the GPU and unequal sequences even out; more make fewer hand-overs of a
+// state. The lengths are on the device: only their mean is known here.
+int linear_segment(int n_seqs, int64_t total_T, int Hv) {
+  const int64_t per_seq = std::max<int64_t>(1, (total_T / std::max(1, n_seqs) + 127) / 128);
+  const int64_t blocks = per_seq * n_seqs * Hv;
+  return (int)std::min<int64_t>(4, std::max<int64_t>(1, (blocks + kLinearCtas - 1) / kLinearCtas));
+}
+
+template <typename T>
+gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const void* v, int64_t total_T,
+                            const float* state_in, gdn::ltc::Params prm, CUtensorMapDataType ty, cudaStream_t st) {
+  const int sms = sm_count();
+  if (sms < 16) return fail(GDN_ERR_CUDA, "%s: cannot query the multiprocessor count", fn);
+  const int64_t items = (total_T / (prm.seg * gdn::ltc::kB) + prm.n_seqs) * prm.Hv;   // at most
+  const int grid = (int)std::min<int64_t>(prm.ws ? INT64_MAX : items, std::min(sms, kLinearCtas));
+  prm.panel = std::min(prm.Hv, gdn::ltc::kScanWarps * grid / gdn::ltc::kSlices);
+  if (!prm.ws) prm.panel = prm.Hv;
+  // about 2 s, and ten times what the blocks take (4000 cycles each)
+  prm.limit = 4000000000ll + (total_T / gdn::ltc::kB + prm.n_seqs) * prm.Hv / grid * 40000;
+  const int64_t states = (int64_t)prm.n_seqs * prm.Hv;
+  CUtensorMap qm, km, vm, om, sim, som;
+  if (!make_map(&qm, q, prm.dk, prm.Hqk, (int)total_T, 64, ty, gdn::ltc::kB) ||
+      !make_map(&km, k, prm.dk, prm.Hqk, (int)total_T, 64, ty, gdn::ltc::kB) ||
+      !make_map(&vm, v, prm.dv, prm.Hv, (int)total_T, 64, ty, gdn::ltc::kB) ||
+      !make_map(&om, prm.o, prm.dv, prm.Hv, (int)total_T, 64, ty, gdn::ltc::kB) ||
+      !make_state_map(&sim, state_in ? state_in : prm.state_out, prm.dk, prm.dv, states) ||
+      !make_state_map(&som, prm.state_out, prm.dk, prm.dv, states))
+    return fail(GDN_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable or failed", fn);
+  auto kern = gdn::ltc::prefill_kernel<T>;
+  if (gdn_status s = allow_smem(kern, fn)) return s;
+  if (prm.ws) {
+    cudaError_t e = cudaMemsetAsync(prm.ws, 0, gdn::ltc::Workspace::flags_bytes(grid), st);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(gdn::ltc::kThreads);
+  cfg.dynamicSmemBytes = gdn::ltc::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;   // with segments CTAs wait on one another: every one co-resident
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = prm.ws ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qm, km, vm, om, sim, som, prm);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return launch_status(fn);
+}
+
 template <typename TS>
 gdn_status linear_decode(const char* fn, const void* q, const void* k, const void* v, const float* g, int g_stride,
                          TS* state, int B, int Hqk, int Hv, int dk, int dv, float scale, gdn_dtype dtype, void* o,
@@ -437,8 +505,12 @@ gdn_status with_pool_types(gdn_code code, gdn_dtype state_dtype, int dk, F f) {
 extern "C" {
 
 size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype) {
-  (void)n_seqs; (void)total_T; (void)Hv; (void)dk; (void)dv; (void)dtype;
-  return 0;
+  (void)dk;
+  (void)dv;
+  if (n_seqs <= 0 || Hv <= 0 || !linear_on_tensor_cores(dtype, total_T)) return 0;
+  // sequences of one segment need none
+  if (total_T <= (int64_t)linear_segment(n_seqs, total_T, Hv) * gdn::ltc::kB) return 0;
+  return gdn::ltc::Workspace::bytes(kLinearCtas);
 }
 
 gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const float* g, int g_stride,
@@ -472,6 +544,32 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
     return fail(GDN_ERR_INVALID_ARG, "%s: workspace needs %zu bytes (16-byte aligned), got %zu", fn, need,
                 workspace_bytes);
   if (scale <= 0.f) scale = 1.0f / sqrtf((float)dk);
+  if (linear_on_tensor_cores(dtype, total_T)) {
+    const int seg = linear_segment(n_seqs, total_T, Hv);
+    if ((total_T / (seg * gdn::ltc::kB) + n_seqs) * Hv > 0x7fff0000)
+      return fail(GDN_ERR_UNSUPPORTED, "%s: %d sequences, %lld tokens, %d heads are more than this kernel schedules", fn,
+                  n_seqs, (long long)total_T, Hv);
+    gdn::ltc::Params prm = {};
+    prm.g = g;
+    prm.state_in = state_in;
+    prm.cu_seqlens = cu_seqlens;
+    prm.o = o;
+    prm.state_out = state_out;
+    prm.ws = need > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
+    prm.g_stride = g_stride;
+    prm.n_seqs = n_seqs;
+    prm.total_T = (int)total_T;
+    prm.Hqk = Hqk;
+    prm.Hv = Hv;
+    prm.dk = dk;
+    prm.dv = dv;
+    prm.seg = seg;
+    prm.scale = scale;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == GDN_F16)
+      return launch_linear_tc<__half>(fn, q, k, v, total_T, state_in, prm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, st);
+    return launch_linear_tc<__nv_bfloat16>(fn, q, k, v, total_T, state_in, prm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, st);
+  }
   return with_dtype(dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
     return with_dk(dk, [&](auto dkc) {
