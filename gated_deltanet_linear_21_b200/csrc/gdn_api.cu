@@ -412,7 +412,7 @@ gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const 
   if (!make_map(&qm, q, prm.dk, prm.Hqk, (int)total_T, 64, ty, gdn::ltc::kB) ||
       !make_map(&km, k, prm.dk, prm.Hqk, (int)total_T, 64, ty, gdn::ltc::kB) ||
       !make_map(&vm, v, prm.dv, prm.Hv, (int)total_T, 64, ty, gdn::ltc::kB) ||
-      !make_map(&om, prm.o, prm.dv, prm.Hv, (int)total_T, 64, ty, gdn::ltc::kB) ||
+      !make_map(&om, prm.o, prm.dv, prm.Hv, (int)total_T, 64, ty, 32) ||
       !make_state_map(&sim, state_in ? state_in : prm.state_out, prm.dk, prm.dv, states) ||
       !make_state_map(&som, prm.state_out, prm.dk, prm.dv, states))
     return fail(GDN_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable or failed", fn);

@@ -8,22 +8,35 @@
 //   P_rs = scale exp(G_r - G_s) q_r . k_s  (s <= r),   o_r = exp(G_r) scale S q_r + sum_s P_rs v_s
 //   S   <- exp(G_L) S + sum_s v_s (exp(G_L - G_s) k_s)^T
 //
-// Four products a block, each 128 x 128 x 128: Q K^T, Q S^T, P V and V^T K~ with
-// K~_s = w_s k_s, w_s = exp(G_L - G_s). No state element ever waits for a sum over
-// tokens outside the tensor core; the state itself lives in fp32 registers of the
-// compute warps (64 values a thread) and is only read by the tensor core as a
-// rounded copy, for o.
+// Four products a block, each 128 x 128 x 128: Q K^T, Q S^T, P V and K~^T V with
+// K~_s = w_s k_s, w_s = exp(G_L - G_s). The state lives, transposed, in fp32 registers
+// of the compute warps (64 values a thread); the tensor core reads a rounded copy of it,
+// for o alone.
 //
 // Precision. o has 16 bits, so P and the copy of S that Q meets are rounded to the
-// input type (half a step each, and no term of o carries both). The state is fp32,
-// so K~ is not rounded: it is split into three bf16 terms (8 bits each, 24 in all)
-// or two f16 terms (22 bits) that are multiplied with V one after another into one
-// accumulator. In f16 powers of two keep what is rounded in the type's range: one from
-// the block's largest |k| and w for the terms of K~, one from the largest |S| for the
-// copy of S, and one for P where a score passes 2^15.
-// Log-decays are summed in fp64 (exp(G_r - G_s) of far tokens is a difference of
-// large sums) and clamped at -200, where exp is zero in fp32, so that a reset (-inf)
-// does not turn differences into NaN.
+// input type (half a step each, and no term of o carries both). The state is fp32, so
+// K~ is not rounded but split into terms that are multiplied with V one after another
+// into one accumulator. With w = w1 + w2 + w3 (each of the input type's precision)
+// packed 16-bit arithmetic gives the terms without leaving the type:
+//
+//   hi = rn(w1 k), e1 = w1 k - hi (exact in one fma), h2 = rn(w2 k), t4 = w3 k + (w2 k - h2)
+//
+// 24 bits in bf16. f16 needs hi and rn(w2 k + e1), 22 bits; in bf16 the same two (16
+// bits) serve where the state is only read for o, inside a segment that is not a
+// sequence's last. In f16 powers of two keep what is rounded in the type's range: one
+// from the block's largest |k| and w for the terms of K~, one from the largest |S| for
+// the copy of S, and one for P where a score passes 2^15.
+// Log-decays are summed in fp64 (exp(G_r - G_s) of far tokens is a difference of large
+// sums) and clamped where exp is zero in fp32, so that a reset (-inf) does not turn
+// differences into NaN. For tokens r, s of different quarters of the block the weight of
+// P is the product of a factor of r and one of s, around the end of s's quarter; inside
+// a quarter it is exp(G_r - G_s) itself.
+//
+// What bounds it. The data move once through HBM at 128 KB a block (fewer where heads
+// share k and q); the products' operands pass shared memory (128 bytes a cycle), which
+// is the tighter bound. So K~'s terms and P are tensor-memory operands: K~ is read from
+// K's tile by ldmatrix with transposition, weighted in registers and stored to tensor
+// memory, and no term ever lies in shared memory.
 //
 // Work over a long axis. Heads alone do not fill the GPU, so a sequence is cut into
 // segments of `seg` blocks; one item is (sequence, head, segment), item i belongs to
@@ -35,17 +48,23 @@
 //      from L2 this time.
 //
 // The states that enter the segments are the running combination of the published
-// ones. Two scan warps per CTA compute it: a warp owns 1/16 of one head's state,
+// ones. Four scan warps per CTA compute it: a warp owns 1/32 of one head's state,
 // carries it in registers from segment to segment and hands every result to the
 // CTA that waits for it. Heads are taken in panels of at most 4 G / 32, so each
 // (head, 1/32) of a panel has an owner of its own.
+//
+// Roles. Warps 0-7 compute. Warp 8 walks the items, hands them to the others through a
+// ring and loads K, V; warp 9 issues the products; warp 10 loads Q and computes the
+// decay tables; warp 11, the courier, waits for and sets the flags in global memory, so
+// that the compute warps wait for none of those; warps 12-15 scan.
 //
 // Order and progress. Items are numbered (sequence, panel, segment, head). Every
 // wait on another CTA is for work of a lower number -- B(i) and scan(i) for scans
 // and publications before i, a publication for the scan of the same slot's last
 // but one user, a scan for the reading of a slot two rounds back -- so with all CTAs
 // resident (cooperative launch) the lowest unfinished one can always go on. All
-// waits are bounded; after one ran out a warp waits no more and runs to its end.
+// waits are bounded, the compute warps' barrier among themselves too; a warp whose wait
+// ran out leaves its loop.
 #pragma once
 
 #include <type_traits>
@@ -61,10 +80,11 @@ using namespace sm100;
 constexpr int kB = 128;              // tokens per block
 constexpr int kD = 128;              // padded head size
 constexpr int kCompute = 256;        // warps 0-7
-constexpr int kLoadWarp = 8;         // K, V tiles
+constexpr int kLoadWarp = 8;         // items; K, V tiles
 constexpr int kMmaWarp = 9;          // tensor-core work
 constexpr int kGateWarp = 10;        // Q tiles and the decay tables
-constexpr int kScanWarp = 12;        // to 15 (warp 11 has no job: registers go by four warps)
+constexpr int kCourierWarp = 11;     // flags in global memory
+constexpr int kScanWarp = 12;        // to 15
 constexpr int kScanWarps = 4;
 constexpr int kThreads = 32 * (kScanWarp + kScanWarps);
 constexpr int kSlices = 32;          // owners of one head's state
@@ -73,38 +93,46 @@ constexpr int kSlices = 32;          // owners of one head's state
 constexpr int kRegsCompute = 176, kRegsOther = 80;
 static_assert(kCompute * kRegsCompute + (kThreads - kCompute) * kRegsOther <= 65536, "register file");
 constexpr int kStateBytes = kD * kD * 4;
-constexpr float kMinLog = -200.f;
+constexpr float kMinLog = -105.f;  // exp is 0 in fp32, subnormals included
 
 // ---- shared memory (bytes) ----
 constexpr uint32_t kQ = 0;                     // [128][128] as two K-major 128B-swizzled atoms, 16 KB apart
 constexpr uint32_t kK = 32768;                 // two buffers
 constexpr uint32_t kV = 98304;                 // two buffers
-constexpr uint32_t kS = 163840;                // the rounded copy of S; pass A: terms of K~, second half
-constexpr uint32_t kML = 196608;               // terms of K~ (half a block); o on its way out
-constexpr uint32_t kStage = kS;                // kS and kML together: a state on its way in or out
-constexpr uint32_t kTab = 229376;              // float w[128], gam[128], gh[128], gl[128]
-constexpr uint32_t kBars = kTab + 2048;
-constexpr uint32_t kMisc = kBars + 256;        // words: see Misc
+constexpr uint32_t kS = 163840;                // the rounded copy of S, [d_k][d_v] as two MN-major atoms
+constexpr uint32_t kO = 196608;                // o on its way out
+constexpr uint32_t kStage = kS;                // kS and kO together: a state on its way in or out
+constexpr uint32_t kTab = 229376;              // w (bf16: words wp1[64], wp2[64], wp3[64]; f16: float[128]), then
+constexpr uint32_t kTabGam = kTab + 768;       // float gam[128], gp[128], gb[128]
+constexpr uint32_t kBars = kTabGam + 1536;
+constexpr uint32_t kRing = kBars + 256;        // items
+constexpr uint32_t kMisc = kRing + 192;        // words: see Misc
 constexpr uint32_t kSmem = kMisc + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
+constexpr int kRingItems = 4;
 
-enum Bar { kKvFull = 0, kKvEmpty = 2, kQFull = 4, kOiDone, kTabFull, kTabEmpty, kPFull, kKt0, kKt1, kMlFree, kPt, kOFull,
-           kOFree, kUFull, kSReady, kStFull, kNumBars };
+enum Bar { kKvFull = 0, kKvEmpty = 2, kItFull = 4, kItEmpty = 8, kQFull = 12, kTabFull, kTabEmpty, kPFull, kKt, kPt, kUFull,
+           kOFull, kStFull, kSlotFree, kPub, kInReady, kGot, kOutOk, kCBar, kNumBars };
+static_assert(kNumBars * 8 <= 256, "barriers");
 
 struct Misc {
   uint32_t tmem;
   float gam_l;         // exp(G_L) of the block
   float seg_gam;       // exp of the segment's total log-decay, up to this block
-  uint32_t big;        // |G| is large somewhere in the block: its low parts are needed
-  float red[8];        // reductions over the compute warps (f16)
   float w_max;         // the largest w of the block
+  float tot[4];        // the quarters' total log-decays (base 2)
+  float red[2][8];     // reductions over the compute warps (f16)
 };
+static_assert(sizeof(Misc) <= 256, "shared memory budget");
 
 // ---- tensor memory columns ----
+// The terms of K~ lie where Q S^T and P V go later in the block: each K half (tokens
+// 0-63, 64-127) in the 64 columns that the warps which write it also read o from.
 constexpr uint32_t kColP = 0;        // Q K^T, then P in place (16 bits: columns 0-31 and 64-95)
-constexpr uint32_t kColOi = 128;     // Q S^T
-constexpr uint32_t kColOa = 256;     // P V
-constexpr uint32_t kColU = 384;      // V^T K~
+constexpr uint32_t kColOi = 128;     // t4, h2; then Q S^T
+constexpr uint32_t kColOa = 256;     // hi, e1 (or the second of two terms); then P V
+constexpr uint32_t kColU = 384;      // K~^T V
+constexpr uint32_t kColHi = kColOa, kColE1 = kColOa + 32, kColT4 = kColOi, kColH2 = kColOi + 32;
 
 // ---- workspace ----
 constexpr int kFlagWords = 32;       // per CTA: out_ready[2], scanned[2], in_cnt[2], done
@@ -135,9 +163,11 @@ struct Wait {
   long long limit;
   bool ok = true;
   __device__ __forceinline__ explicit Wait(long long l) : limit(l) {}
+  // by the whole warp, which agrees on the outcome
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait(bar, parity, limit);
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, limit));
   }
+  // by one lane
   __device__ __forceinline__ void flag(const uint32_t* p, uint32_t target) {
     if (ok) ok = wait_flag_geq(p, target, limit);
   }
@@ -149,6 +179,8 @@ struct Item {
   int t0, len;         // the segment's first token and tokens
   int first;           // the item of segment 0 of this sequence and head
 };
+
+static_assert(sizeof(Item) * kRingItems <= 192, "shared memory budget");
 
 // Finds items in increasing order (warp-collective).
 struct Walk {
@@ -205,6 +237,51 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* u) {
       "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
 }
+// 16 lanes x 32 columns, as 8 x 8 matrices of 16-bit pairs: u[2 i + b] of thread t is row
+// 8 b + t / 4 of the lanes, column 4 i + t % 4.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, transposed: thread t holds rows 2 (t % 4) and + 1 of
+// column t / 4 of each.
+__device__ __forceinline__ void ldmatrix_t4(uint32_t saddr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+// Packed arithmetic on two values of the 16-bit type, rounded to nearest even.
+template <typename T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+  }
+};
+template <> struct Two<__half> {
+  static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+  }
+};
+__device__ __forceinline__ uint32_t neg2(uint32_t a) { return a ^ 0x80008000u; }
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four K-steps with A in TMEM (8 columns a step) and B advancing BSTEP 16-byte units a
@@ -269,14 +346,15 @@ __device__ __forceinline__ void scan_role(const Params& p, int ow, int G) {
           const int hp = min(p.panel, p.Hv - h0);
           if (hl >= hp) continue;
           float4 S[4];
-          // word x = v * 256 + t of a slot holds columns 4 v .. 4 v + 3 of thread t's 64
+          // word x = v * 256 + t of a slot holds rows (d_v) 64 (t / 128) + 4 v .. + 3 of column t % 128
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int t = 128 * (sl & 1) + 32 * u + lane, row = t & 127, col = 64 * (t >> 7) + 4 * (sl >> 1);
+            const int t = 128 * (sl & 1) + 32 * u + lane, col = t & 127, row = 64 * (t >> 7) + 4 * (sl >> 1);
             S[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.state_in && row < p.dv && col < p.dk)
-              S[u] = __ldcg(reinterpret_cast<const float4*>(
-                  p.state_in + (((size_t)(n0 + i) * p.Hv + h0 + hl) * p.dv + row) * p.dk + col));
+            if (p.state_in && row < p.dv && col < p.dk) {   // (d_v is a multiple of 4)
+              const float* x = p.state_in + (((size_t)(n0 + i) * p.Hv + h0 + hl) * p.dv + row) * p.dk + col;
+              S[u] = make_float4(__ldcg(x), __ldcg(x + p.dk), __ldcg(x + 2 * p.dk), __ldcg(x + 3 * p.dk));
+            }
           }
           for (int j = 0; j + 1 < Jn; ++j) {
             const int item = base + h0 * Jn + j * hp + hl, c = item % G, r = item / G;
@@ -327,14 +405,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
                const __grid_constant__ CUtensorMap sim, const __grid_constant__ CUtensorMap som, const Params p) {
   constexpr bool kF16 = std::is_same<T, __half>::value;
   constexpr uint32_t kFmt = Op16<T>::kFmt;
-  constexpr int kTerms = kF16 ? 2 : 3;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kBars);
   Misc* misc = reinterpret_cast<Misc*>(sm + kMisc);
-  float* tab_w = reinterpret_cast<float*>(sm + kTab);
-  float* tab_gam = tab_w + kB;
-  float* tab_gh = tab_w + 2 * kB;
-  float* tab_gl = tab_w + 3 * kB;
+  Item* ring = reinterpret_cast<Item*>(sm + kRing);
+  uint32_t* tab_wp = reinterpret_cast<uint32_t*>(sm + kTab);    // bf16: three words of pairs
+  float* tab_w = reinterpret_cast<float*>(sm + kTab);           // f16
+  float* tab_gam = reinterpret_cast<float*>(sm + kTabGam);      // exp(G_r) scale
+  float* tab_gp = tab_gam + kB;                                 // log2 decay from the start of r's quarter to r
+  float* tab_gb = tab_gam + 2 * kB;                             // exp of the decay from s to the end of its quarter
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = gridDim.x, cta = blockIdx.x;
 
@@ -344,8 +423,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   }
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool warps = i == kTabEmpty || i == kKt0 || i == kKt1 || i == kPt || i == kOFree || i == kSReady;
-      mbar_init(&bars[i], warps ? 8 : i == kTabFull ? 32 : 1);
+      const bool warps = i == kTabEmpty || i == kKt || i == kPt || i == kPub || i == kGot || i == kCBar;
+      const bool readers = i >= kItEmpty && i < kItEmpty + kRingItems;
+      mbar_init(&bars[i], warps ? 8 : readers ? (p.ws ? 11 : 10) : 1);
     }
     fence_mbar_init();
   }
@@ -359,14 +439,30 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   const uint32_t tmem = misc->tmem;
   const uint32_t sbase = smem_u32(sm);
   Wait wait(p.limit);
-  Walk walk;
+  // the CTA's i-th item, false behind the last
+  auto next_item = [&](uint32_t i, Item& it) {
+    wait(&bars[kItFull + (i & 3)], (i >> 2) & 1);
+    if (!wait.ok) return false;
+    it = ring[i & 3];
+    arrive_warp(&bars[kItEmpty + (i & 3)]);
+    return it.n >= 0;
+  };
   Item it;
+
   if (warp == kLoadWarp) {
     give_registers();
-    // ---------------------------------------------------------- K, V tiles ---
+    // ------------------------------------------------- items; K, V tiles ---
     const uint64_t once = l2_evict_first_policy();
+    Walk walk;
     uint32_t cnt = 0;
-    for (int item = cta; walk.find(p, item, it); item += G) {
+    bool more = true;
+    for (uint32_t i = 0; more && wait.ok; ++i) {
+      more = walk.find(p, cta + (int)i * G, it);
+      if (!more) it.n = -1;
+      if (i >= kRingItems) wait(&bars[kItEmpty + (i & 3)], ((i >> 2) - 1) & 1);
+      if (lane == 0) ring[i & 3] = it;
+      arrive_warp(&bars[kItFull + (i & 3)]);
+      if (!more) break;
       const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
       const bool shared_k = p.Hv != p.Hqk;
       for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
@@ -402,11 +498,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     give_registers();
     // ------------------------------------------- Q tiles and decay tables ---
     uint32_t qn = 0, tn = 0;
-    for (int item = cta; walk.find(p, item, it); item += G) {
+    for (uint32_t i = 0; next_item(i, it); ++i) {
       const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
       for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
         double seg = 0.0;
-        for (int b = 0; b < nb; ++b) {
+        for (int b = 0; b < nb && wait.ok; ++b) {
           const int t = it.t0 + b * kB, L = min(kB, it.len - b * kB);
           float x[4];
 #pragma unroll
@@ -416,7 +512,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             x[e] = gv < kMinLog ? kMinLog : gv;
           }
           if (pass == 1) {
-            if (qn > 0) wait(&bars[kOiDone], (qn - 1) & 1);
+            if (qn > 0) wait(&bars[kOFull], (qn - 1) & 1);
             if (wait.ok) {
               mbar_arrive_expect_tx_warp(&bars[kQFull], 32768);
               tma_load_3d_warp(sm + kQ, &qm, &bars[kQFull], 0, hq, t);
@@ -433,36 +529,44 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             if (lane >= off) incl += y;
           }
           const double end = __shfl_sync(0xffffffffu, incl, 31), before = incl - c[3];
+          const double q0 = __shfl_sync(0xffffffffu, before, lane & 24), q1 = __shfl_sync(0xffffffffu, incl, lane | 7);
           seg += end;
-          float w[4], gm[4], gh[4], gl[4], far = 0.f;
+          float w[4], gm[4], gp[4], gb[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const double Gs = before + c[e], G2 = Gs * 1.4426950408889634;
+            const double Gs = before + c[e];
             w[e] = 4 * lane + e < L ? expf((float)(end - Gs)) : 0.f;
             gm[e] = expf((float)Gs) * p.scale;
-            gh[e] = (float)G2;
-            gl[e] = (float)(G2 - (double)gh[e]);
-            far = fmaxf(far, fabsf(gh[e]));
+            gp[e] = (float)((Gs - q0) * 1.4426950408889634);
+            gb[e] = expf((float)(q1 - Gs));
           }
-          // from 64 on half a step of gh alone would move a weight by 2.6e-6 of itself
-          const uint32_t big = __any_sync(0xffffffffu, !(far < 64.f));
-          if (tn > 0) wait(&bars[kTabEmpty], (tn - 1) & 1);
-          reinterpret_cast<float4*>(tab_w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<float4*>(tab_gam)[lane] = make_float4(gm[0], gm[1], gm[2], gm[3]);
-          reinterpret_cast<float4*>(tab_gh)[lane] = make_float4(gh[0], gh[1], gh[2], gh[3]);
-          reinterpret_cast<float4*>(tab_gl)[lane] = make_float4(gl[0], gl[1], gl[2], gl[3]);
           float wm = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
           if constexpr (kF16) {
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
           }
+          if (tn > 0) wait(&bars[kTabEmpty], (tn - 1) & 1);
+          if constexpr (kF16) {
+            reinterpret_cast<float4*>(tab_w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              const uint32_t lo = Op16<T>::pack2(w[0], w[1]), hi = Op16<T>::pack2(w[2], w[3]);
+              reinterpret_cast<uint2*>(tab_wp + 64 * term)[lane] = make_uint2(lo, hi);
+              const float2 a = Op16<T>::unpack2(lo), d = Op16<T>::unpack2(hi);
+              w[0] -= a.x; w[1] -= a.y; w[2] -= d.x; w[3] -= d.y;
+            }
+          }
+          reinterpret_cast<float4*>(tab_gam)[lane] = make_float4(gm[0], gm[1], gm[2], gm[3]);
+          reinterpret_cast<float4*>(tab_gp)[lane] = make_float4(gp[0], gp[1], gp[2], gp[3]);
+          reinterpret_cast<float4*>(tab_gb)[lane] = make_float4(gb[0], gb[1], gb[2], gb[3]);
+          if ((lane & 7) == 0) misc->tot[lane >> 3] = (float)((q1 - q0) * 1.4426950408889634);
           if (lane == 0) {
             misc->w_max = wm;
             misc->gam_l = expf((float)end);
             misc->seg_gam = expf((float)seg);
-            misc->big = big;
           }
-          mbar_arrive(&bars[kTabFull]);
+          arrive_warp(&bars[kTabFull]);
           ++tn;
         }
       }
@@ -471,102 +575,130 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   } else if (warp == kMmaWarp) {
     give_registers();
     // ------------------------------------------------- tensor-core work ---
-    constexpr uint32_t id_kk = idesc_f16kind(128, 128, false, false, kFmt);
-    constexpr uint32_t id_pv = idesc_f16kind(128, 128, false, true, kFmt);
-    constexpr uint32_t id_u = idesc_f16kind(128, 128, true, true, kFmt);
-    uint32_t cnt = 0, qn = 0, un = 0, bn = 0;
-    for (int item = cta; walk.find(p, item, it); item += G) {
+    constexpr uint32_t id_qk = idesc_f16kind(128, 128, false, false, kFmt);   // both K-major
+    constexpr uint32_t id_mn = idesc_f16kind(128, 128, false, true, kFmt);    // B MN-major
+    uint32_t cnt = 0, qn = 0, un = 0;
+    for (uint32_t i = 0; next_item(i, it); ++i) {
       const int nb = (it.len + kB - 1) / kB;
       const bool last = it.j + 1 == it.J;
       for (int pass = last ? 1 : 0; pass < 2; ++pass) {
-        for (int b = 0; b < nb; ++b, ++cnt) {
+        for (int b = 0; b < nb && wait.ok; ++b, ++cnt) {
           const uint32_t s = cnt & 1;
-          const uint32_t kt = sbase + kK + s * 32768, vt = sbase + kV + s * 32768;
+          const uint32_t kt = sbase + kK + s * 32768;
+          const uint64_t vd = desc_mnmajor(sbase + kV + s * 32768, 0, 128, 16384);
+          const uint64_t vd4 = desc_advance(vd, 4 * 2048);
           const bool upd = pass == 0 || last || b + 1 < nb;   // the state after the segment comes from pass A
+          const bool four = !kF16 && (pass == 0 || last);
           wait(&bars[kKvFull + s], (cnt >> 1) & 1);
           if (pass == 1) {
             wait(&bars[kQFull], qn & 1);
             tc_fence_after();
-            {
-              const uint64_t qd = desc_kmajor(sbase + kQ, 0, 16384), kd = desc_kmajor(kt, 0, 16384);
-              mma_run_warp<4, 2, 2>(tmem + kColP, qd, kd, id_kk, 0);
-              mma_run_warp<4, 2, 2>(tmem + kColP, desc_advance(qd, 16384), desc_advance(kd, 16384), id_kk, 1);
-            }
+            const uint64_t qd = desc_kmajor(sbase + kQ, 0, 16384), kd = desc_kmajor(kt, 0, 16384);
+            mma_run_warp<4, 2, 2>(tmem + kColP, qd, kd, id_qk, 0);
+            mma_run_warp<4, 2, 2>(tmem + kColP, desc_advance(qd, 16384), desc_advance(kd, 16384), id_qk, 1);
             mma_commit_warp(&bars[kPFull]);
-            wait(&bars[kSReady], qn & 1);
-            if (qn > 0) wait(&bars[kOFree], (qn - 1) & 1);
-            tc_fence_after();
-            {
-              const uint64_t qd = desc_kmajor(sbase + kQ, 0, 16384), sd = desc_kmajor(sbase + kS, 0, 16384);
-              mma_run_warp<4, 2, 2>(tmem + kColOi, qd, sd, id_kk, 0);
-              mma_run_warp<4, 2, 2>(tmem + kColOi, desc_advance(qd, 16384), desc_advance(sd, 16384), id_kk, 1);
-            }
-            mma_commit_warp(&bars[kOiDone]);
-            ++qn;
-          }
-          auto half = [&](int hf, uint32_t buf) {
-            wait(&bars[kKt0 + hf], un & 1);
-            tc_fence_after();
-            const uint64_t vd = desc_mnmajor(vt, 4 * hf, 128, 16384);
-            mma_run_warp<4, 128, 128>(tmem + kColU, vd, desc_mnmajor(kt, 4 * hf, 128, 16384), id_u, hf);
-#pragma unroll
-            for (int term = 1; term < kTerms; ++term)
-              mma_run_warp<4, 128, 128>(tmem + kColU, vd, desc_mnmajor(buf + (term - 1) * 16384, 0, 128, 8192), id_u, 1);
-          };
-          if (upd) half(0, sbase + kML);
-          if (pass == 1) {
-            if (upd) mma_commit_warp(&bars[kMlFree]);
-            wait(&bars[kPt], bn++ & 1);
-            tc_fence_after();
-            {
-              const uint64_t vd = desc_mnmajor(vt, 0, 128, 16384);
-              mma4_tmem_a_run_warp<128>(tmem + kColOa, tmem + kColP, vd, id_pv, 0);
-              mma4_tmem_a_run_warp<128>(tmem + kColOa, tmem + kColP + 64, desc_advance(vd, 4 * 2048), id_pv, 1);
-            }
-            mma_commit_warp(&bars[kOFull]);
           }
           if (upd) {
-            half(1, pass == 0 ? sbase + kS : sbase + kML);
-            ++un;
+            wait(&bars[kKt], un++ & 1);
+            tc_fence_after();
+            auto term = [&](uint32_t col, uint32_t acc) {
+              mma4_tmem_a_run_warp<128>(tmem + kColU, tmem + col, vd, id_mn, acc);
+              mma4_tmem_a_run_warp<128>(tmem + kColU, tmem + col + 64, vd4, id_mn, 1);
+            };
+            term(kColE1, 0);
+            if (four) {
+              term(kColH2, 1);
+              term(kColT4, 1);
+            }
+            term(kColHi, 1);
             mma_commit_warp(&bars[kUFull]);
+          }
+          if (pass == 1) {
+            wait(&bars[kPt], qn & 1);
+            tc_fence_after();
+            const uint64_t qd = desc_kmajor(sbase + kQ, 0, 16384), sd = desc_mnmajor(sbase + kS, 0, 128, 16384);
+            mma_run_warp<4, 2, 128>(tmem + kColOi, qd, sd, id_mn, 0);
+            mma_run_warp<4, 2, 128>(tmem + kColOi, desc_advance(qd, 16384), desc_advance(sd, 4 * 2048), id_mn, 1);
+            mma4_tmem_a_run_warp<128>(tmem + kColOa, tmem + kColP, vd, id_mn, 0);
+            mma4_tmem_a_run_warp<128>(tmem + kColOa, tmem + kColP + 64, vd4, id_mn, 1);
+            mma_commit_warp(&bars[kOFull]);
+            ++qn;
           }
           mma_commit_warp(&bars[kKvEmpty + s]);
         }
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp == kCourierWarp) {
+    give_registers();
+    // ---------------------------------------------- flags in global memory ---
+    if (p.ws) {
+      uint32_t* all = reinterpret_cast<uint32_t*>(p.ws);
+      uint32_t* flags = all + cta * kFlagWords;
+      uint32_t pubs0 = 0, pubs1 = 0, ins0 = 0, ins1 = 0, pn = 0;   // uses of this CTA's slots, by parity
+      for (uint32_t i = 0; next_item(i, it); ++i) {
+        const int par = i & 1;
+        const bool last = it.j + 1 == it.J;
+        if (!last) {
+          const uint32_t used = par ? pubs1++ : pubs0++;
+          if (lane == 0 && used > 0) wait.flag(flags + kScanned + par, kSlices * used);
+          arrive_warp(&bars[kSlotFree]);
+          wait(&bars[kPub], pn++ & 1);
+          if (lane == 0) {
+            fence_acq_rel_gpu();
+            st_release_gpu(flags + kOutReady + par, i + 1);
+          }
+        }
+        if (it.j > 0) {
+          const uint32_t use = par ? ++ins1 : ++ins0;
+          if (lane == 0) wait.flag(flags + kInCnt + par, kSlices * use);
+          arrive_warp(&bars[kInReady]);
+        }
+        wait(&bars[kGot], i & 1);
+        if (lane == 0) {
+          fence_acq_rel_gpu();
+          st_release_gpu(flags + kDone, i + 1);
+        }
+        if (last && it.J > 1) {
+          // state_out may be state_in, whose reader is then the first segment
+          if (lane == 0) wait.flag(all + (it.first % G) * kFlagWords + kDone, it.first / G + 1);
+          arrive_warp(&bars[kOutOk]);
+        }
+      }
+    }
+  } else if (warp >= kScanWarp) {
     give_registers();
     // ------------------------------------- states between the segments ---
-    if (p.ws && warp >= kScanWarp) scan_role(p, cta * kScanWarps + warp - kScanWarp, G);
+    if (p.ws) scan_role(p, cta * kScanWarps + warp - kScanWarp, G);
   } else {
-    // ----------------------------------------------------- compute warps ---
     take_registers();
-    const int wg = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;   // row of every 128-row tile, columns 64 wg ..
+    // ----------------------------------------------------- compute warps ---
+    // Warp w4 of each half wg has lanes 32 w4 .. of tensor memory: rows (tokens) of P and
+    // o, columns (d_k) of K~ and of the state. wg: the half of the tokens of K~, of the
+    // columns of P, and of d_v in o and the state.
+    const int wg = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w4) << 16);
-    uint32_t* flags = reinterpret_cast<uint32_t*>(p.ws) + cta * kFlagWords;
     float* meta = reinterpret_cast<float*>(p.ws + Workspace::meta_offset(G)) + 2 * cta;
     uint8_t* slots = p.ws + Workspace::slots_offset(G) + (size_t)cta * 4 * kStateBytes;
     const float log2_scale = log2f(p.scale);
-    uint32_t cnt = 0, tn = 0, qn = 0, un = 0, mn = 0, stn = 0;
-    uint32_t pubs0 = 0, pubs1 = 0, ins0 = 0, ins1 = 0;   // uses of this CTA's slots, by parity
-    float S[64];
+    uint32_t cnt = 0, tn = 0, qn = 0, un = 0, stn = 0, pn = 0, inn = 0, okn = 0, bn = 0, rn = 0;
+    float S[64];        // S[64 wg + i][row]
     float s_up = 1.f;   // f16: the copy of S is S / s_up
 
-    // kS and kML may be written again: earlier bulk stores have read them
-    auto acquire_stage = [&] {
-      if (tid == 0) bulk_wait_read_all();
-      named_bar_sync(1, kCompute);
+    // the compute warps' barrier
+    auto sync = [&] {
+      arrive_warp(&bars[kCBar]);
+      wait(&bars[kCBar], bn++ & 1);
     };
     // the largest value over the compute threads (f16)
     auto reduce_max = [&](float m) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      if (lane == 0) misc->red[warp] = m;
-      named_bar_sync(1, kCompute);
-      m = misc->red[0];
+      float* red = misc->red[rn++ & 1];   // (the one used two reductions ago: a barrier lies between)
+      if (lane == 0) red[warp] = m;
+      sync();
+      m = red[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, misc->red[i]);
-      named_bar_sync(1, kCompute);
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
       return m;
     };
     // the rounded copy of S
@@ -588,54 +720,87 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         *reinterpret_cast<uint4*>(sm + kS + wg * 16384 + row * 128 + ((c ^ (row & 7)) << 4)) = pack8<T>(x);
       }
       fence_async_smem();
-      arrive_warp(&bars[kSReady]);
     };
-    // K~'s terms for tokens 64 hf .. 64 hf + 63 of the block: the first over K itself
-    auto make_terms = [&](int hf, uint32_t kt, uint32_t buf, float up) {
+    // The terms of K~ for tokens 64 wg .. + 63 and columns 32 w4 .. + 31 of K's tile at kt.
+    // Returns the power of two that they were multiplied with (f16).
+    const uint32_t ldm_row = 64 * wg + 8 * ((lane >> 4) & 1) + (lane & 7);
+    auto make_terms = [&](uint32_t kt, int L, bool four) -> int {
+      uint32_t kr[32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (tid >> 4) + 16 * i, c = tid & 15;         // token in the half, 16-byte chunk
-        const uint32_t in_row = ((c & 7) ^ (r & 7)) << 4;
-        uint4* src = reinterpret_cast<uint4*>(sm + kt + (c >> 3) * 16384 + (64 * hf + r) * 128 + in_row);
-        uint8_t* dst = sm + buf + (c >> 3) * 8192 + r * 128 + in_row;
-        const float w = tab_w[64 * hf + r] * (kF16 ? up : 1.f);
-        float x[8], y[8];
-        unpack8<T>(*src, x);
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t c = 4 * w4 + 2 * half + ((lane >> 3) & 1);     // 16-byte chunk of K's row
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = w != 0.f ? x[e] * w : 0.f;   // (rows behind the sequence may hold anything)
+        for (int i = 0; i < 8; i += 2) {
+          const uint32_t r = ldm_row + 8 * i;
+          ldmatrix_t4(sbase + kt + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), kr + 16 * half + 2 * i);
+        }
+      }
+      if (L < kB) {   // rows behind the sequence may hold anything
 #pragma unroll
-        for (int term = 0; term < kTerms; ++term) {
-          const uint4 v = pack8<T>(x);
-          if (term == 0)
-            *src = v;
-          else
-            *reinterpret_cast<uint4*>(dst + (term - 1) * 16384) = v;
-          if (term + 1 < kTerms) {
-            unpack8<T>(v, y);
+        for (int i = 0; i < 8; ++i) {
+          const int t = 64 * wg + 8 * i + 2 * (lane & 3);
+          const uint32_t keep = (t < L ? 0xffffu : 0u) | (t + 1 < L ? 0xffff0000u : 0u);
+          kr[2 * i] &= keep; kr[2 * i + 1] &= keep; kr[16 + 2 * i] &= keep; kr[17 + 2 * i] &= keep;
+        }
+      }
+      uint32_t w1[8], w2[8], w3[8];
+      int e = 0;
+      if constexpr (kF16) {
+        __half2 m = __half2half2(__ushort_as_half(0));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] -= y[e];
+        for (int i = 0; i < 32; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<__half2*>(&kr[i])));
+        const float2 f = __half22float2(m);
+        // |w k| below 2^14 and w below 2^15
+        e = min(13 - exponent_of(reduce_max(fmaxf(f.x, f.y)) * misc->w_max), 14 - exponent_of(misc->w_max));
+        const float up = pow2i(e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float2 w = *reinterpret_cast<const float2*>(tab_w + 64 * wg + 8 * i + 2 * (lane & 3));
+          w.x *= up; w.y *= up;
+          w1[i] = Op16<T>::pack2(w.x, w.y);
+          const float2 x = Op16<T>::unpack2(w1[i]);
+          w2[i] = Op16<T>::pack2(w.x - x.x, w.y - x.y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t at = 32 * wg + 4 * i + (lane & 3);
+          w1[i] = tab_wp[at];
+          w2[i] = tab_wp[64 + at];
+          w3[i] = tab_wp[128 + at];
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t tw = tl + (static_cast<uint32_t>(16 * half) << 16) + 64 * wg;
+        uint32_t x[16], y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          x[i] = Two<T>::mul(w1[i >> 1], kr[16 * half + i]);
+          y[i] = Two<T>::fma(w1[i >> 1], kr[16 * half + i], neg2(x[i]));
+        }
+        tmem_st_frag(tw + kColHi, x);
+        if (four) {
+          tmem_st_frag(tw + kColE1, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = Two<T>::mul(w2[i >> 1], kr[16 * half + i]);
+          tmem_st_frag(tw + kColH2, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            y[i] = Two<T>::fma(w2[i >> 1], kr[16 * half + i], neg2(x[i]));
+            if constexpr (!kF16) y[i] = Two<T>::fma(w3[i >> 1], kr[16 * half + i], y[i]);
           }
+          tmem_st_frag(tw + kColT4, y);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = Two<T>::fma(w2[i >> 1], kr[16 * half + i], y[i]);
+          tmem_st_frag(tw + kColE1, y);
         }
       }
-      fence_async_smem();
-      arrive_warp(&bars[kKt0 + hf]);
-    };
-    // f16: the power of two that brings the block's |w k| below 2^14
-    auto term_scale = [&](uint32_t kt, int L) {
-      __half2 m = __half2half2(__ushort_as_half(0));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = (tid >> 4) + 16 * i, c = tid & 15;
-        if (r < L) {
-          const uint4 v =
-              *reinterpret_cast<const uint4*>(sm + kt + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(h[e]));
-        }
-      }
-      const float2 f = __half22float2(m);
-      return exponent_of(reduce_max(fmaxf(f.x, f.y)) * misc->w_max) - 13;
+      tmem_wait_st();
+      tc_fence_before();
+      arrive_warp(&bars[kKt]);
+      return e;
     };
     // rows of V behind the sequence: zero (their weights are, but they may hold anything)
     auto clear_v = [&](uint32_t vt, int L) {
@@ -658,51 +823,142 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       }
       tc_fence_before();
     };
+    // P, packed, over Q K^T. Returns the power of two that it was divided by (f16).
+    auto make_scores = [&](int L) -> float {
+      const float gr = tab_gp[row] + log2_scale;
+      uint32_t u[32];
+      auto scores = [&](float down) {
+        float top = 0.f, far = 0.f;
+#pragma unroll
+        for (int c = 1; c >= 0; --c) {
+          const int cb = 2 * wg + c;               // columns 32 cb ..: zero above the diagonal
+          if (cb > w4) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[16 * c + i] = 0u;
+            continue;
+          }
+          float x[32];
+          tmem_ld32(tl + kColP + 32 * cb, x);
+          if (cb == w4) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 h4 = *reinterpret_cast<const float4*>(tab_gp + 32 * cb + i);
+              const float d[4] = {gr - h4.x, gr - h4.y, gr - h4.z, gr - h4.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) x[i + y] = i + y <= lane ? x[i + y] * ex2(d[y]) : 0.f;
+            }
+          } else {
+            far = 0.f;
+            for (int y = cb + 1; y < w4; ++y) far += misc->tot[y];
+            const float a = ex2(gr + far);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 b4 = *reinterpret_cast<const float4*>(tab_gb + 32 * cb + i);
+              x[i] *= b4.x * a; x[i + 1] *= b4.y * a; x[i + 2] *= b4.z * a; x[i + 3] *= b4.w * a;
+            }
+          }
+          if constexpr (kF16) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              top = fmaxf(top, fabsf(x[i]));
+              x[i] *= down;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[16 * c + i] = Op16<T>::pack2(x[2 * i], x[2 * i + 1]);
+        }
+        return row < L ? top : 0.f;
+      };
+      const float top = scores(1.f);
+      float up = 1.f;
+      if constexpr (kF16) {
+        const float most = reduce_max(top);
+        if (most >= 32768.f) {
+          const int e = exponent_of(most) - 14;
+          up = pow2i(e);
+          scores(pow2i(-e));
+        }
+      }
+      tmem_st16(tl + kColP + 64 * wg, u);
+      tmem_st16(tl + kColP + 64 * wg + 16, u + 16);
+      tmem_wait_st();
+      tc_fence_before();
+      arrive_warp(&bars[kPt]);
+      return up;
+    };
+    // o of this warp's 32 tokens and 64 columns, through its own part of kO
+    uint8_t* o_stage = sm + kO + wg * 16384 + w4 * 4096;
+    const int o_chunks = min(8, max(0, p.dv / 8 - 8 * wg));    // 16-byte chunks of these columns
+    auto write_o = [&](int t, int h, int L, float row_gam, float up) {
+      if (o_chunks == 0) return;
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float x[16], y[16];
+        tmem_ld16(tl + kColOi + 64 * wg + 16 * c, x);
+        tmem_ld16(tl + kColOa + 64 * wg + 16 * c, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = fmaf(row_gam, x[i], kF16 ? y[i] * up : y[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint4*>(o_stage + lane * 128 + (((2 * c + i) ^ (lane & 7)) << 4)) = pack8<T>(x + 8 * i);
+      }
+      tc_fence_before();
+      const int rows = min(32, L - 32 * w4);
+      if (rows == 32) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&om, o_stage, 64 * wg, h, t + 32 * w4);
+          bulk_commit_group();
+        }
+      } else {
+        __syncwarp();
+        T* o = static_cast<T*>(p.o);
+        for (int i = lane; i < rows * o_chunks; i += 32) {
+          const int r = i / o_chunks, c = i - r * o_chunks;
+          __stcs(reinterpret_cast<uint4*>(o + ((size_t)(t + 32 * w4 + r) * p.Hv + h) * p.dv + 64 * wg + 8 * c),
+                 *reinterpret_cast<const uint4*>(o_stage + r * 128 + ((c ^ (r & 7)) << 4)));
+        }
+      }
+    };
+    // element (d_v 64 wg + i, d_k row) of a staged state: boxes of 32 columns, 128-byte rows
+    auto staged = [&](int i) {
+      const int v = 64 * wg + i;
+      return reinterpret_cast<float*>(sm + kStage + w4 * 16384 + v * 128 + (((lane >> 2) ^ (v & 7)) << 4) + (lane & 3) * 4);
+    };
 
-    for (int item = cta; walk.find(p, item, it); item += G) {
-      const int nb = (it.len + kB - 1) / kB, r = item / G, par = r & 1;
+    for (uint32_t i = 0; next_item(i, it); ++i) {
+      const int nb = (it.len + kB - 1) / kB, par = i & 1;
       const bool last = it.j + 1 == it.J;
       if (!last) {
         // --------------------------------------------------------- pass A ---
-        acquire_stage();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = 0.f;
+        for (int x = 0; x < 64; ++x) S[x] = 0.f;
         float seg_gam = 1.f;
-        for (int b = 0; b < nb; ++b, ++cnt) {
-          const uint32_t s = cnt & 1, kt = kK + s * 32768;
-          const int L = min(kB, it.len - b * kB);   // (only a last segment has a short block)
+        for (int b = 0; b < nb && wait.ok; ++b, ++cnt) {
+          const uint32_t s = cnt & 1;
           wait(&bars[kTabFull], tn++ & 1);
           wait(&bars[kKvFull + s], (cnt >> 1) & 1);
           const float gam = misc->gam_l;
           seg_gam = misc->seg_gam;
-          int e = 0;
-          if constexpr (kF16) e = term_scale(kt, L);
-          make_terms(0, kt, kML, pow2i(-e));
-          make_terms(1, kt, kS, pow2i(-e));
+          const int e = make_terms(kK + s * 32768, kB, !kF16);   // (only a last segment has a short block)
           arrive_warp(&bars[kTabEmpty]);
-          update_state(gam, pow2i(e));
+          update_state(gam, pow2i(-e));
         }
-        const uint32_t used = par ? pubs1++ : pubs0++;
-        if (tid == 0 && used > 0) wait.flag(flags + kScanned + par, kSlices * used);
-        named_bar_sync(1, kCompute);
+        wait(&bars[kSlotFree], pn++ & 1);
         float4* out = reinterpret_cast<float4*>(slots + (size_t)par * kStateBytes);
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           __stcg(out + 256 * v + tid, make_float4(S[4 * v], S[4 * v + 1], S[4 * v + 2], S[4 * v + 3]));
         if (tid == 0) __stcg(meta + par, seg_gam);
-        named_bar_sync(1, kCompute);
-        if (tid == 0) {
-          fence_acq_rel_gpu();
-          st_release_gpu(flags + kOutReady + par, r + 1);
-        }
+        arrive_warp(&bars[kPub]);
       }
       // ----------------------------------------------------------- pass B ---
       // the state that enters
-      acquire_stage();
       if (it.j > 0) {
-        const uint32_t use = par ? ++ins1 : ++ins0;
-        if (lane == 0) wait.flag(flags + kInCnt + par, kSlices * use);
-        __syncwarp();
+        wait(&bars[kInReady], inn++ & 1);
         const float4* in = reinterpret_cast<const float4*>(slots + (size_t)(2 + par) * kStateBytes);
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
@@ -711,8 +967,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         }
       } else if (p.state_in) {
         const int boxes = (p.dk + 31) / 32;
+        if (lane == 0) bulk_wait_read_all();   // (what went out through kS and kO)
         fence_async_smem();
-        named_bar_sync(1, kCompute);
+        sync();
         if (tid == 0) {
           mbar_arrive_expect_tx(&bars[kStFull], boxes * 16384);
           for (int x = 0; x < boxes; ++x)
@@ -720,154 +977,50 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         }
         wait(&bars[kStFull], stn++ & 1);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const int x = 2 * wg + (c >> 3);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (x < boxes)
-            v = *reinterpret_cast<const float4*>(sm + kStage + x * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-          S[4 * c] = v.x; S[4 * c + 1] = v.y; S[4 * c + 2] = v.z; S[4 * c + 3] = v.w;
-        }
-        named_bar_sync(1, kCompute);
+        for (int x = 0; x < 64; ++x) S[x] = w4 < boxes ? *staged(x) : 0.f;
+        sync();
       } else {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = 0.f;
+        for (int x = 0; x < 64; ++x) S[x] = 0.f;
       }
-      if (nb > 0) write_copy();
-      if (p.ws) {
-        named_bar_sync(1, kCompute);   // every thread has its part
-        if (tid == 0) st_release_gpu(flags + kDone, r + 1);
+      if (nb > 0) {
+        // kS may be a state's on its way out (thread 0's stores)
+        if (i > 0 && !(it.j == 0 && p.state_in)) {
+          if (tid == 0) bulk_wait_read_all();
+          sync();
+        }
+        write_copy();
       }
-      for (int b = 0; b < nb; ++b, ++cnt, ++qn) {
-        const uint32_t s = cnt & 1, kt = kK + s * 32768, vt = kV + s * 32768;
+      if (p.ws) arrive_warp(&bars[kGot]);
+      for (int b = 0; b < nb && wait.ok; ++b, ++cnt, ++qn) {
+        const uint32_t s = cnt & 1;
         const int t = it.t0 + b * kB, L = min(kB, it.len - b * kB);
         const bool upd = last || b + 1 < nb;
         wait(&bars[kTabFull], tn++ & 1);
         wait(&bars[kKvFull + s], (cnt >> 1) & 1);
         const float gam = misc->gam_l, row_gam = tab_gam[row] * s_up;
-        const bool big = misc->big != 0;
-        if (L < kB) clear_v(vt, L);
+        if (L < kB) clear_v(kV + s * 32768, L);
         int e = 0;
-        if constexpr (kF16) {
-          if (upd) e = term_scale(kt, L);
-        }
-        acquire_stage();
+        if (upd) e = make_terms(kK + s * 32768, L, !kF16 && last);
         wait(&bars[kPFull], qn & 1);
         tc_fence_after();
-        if (upd) make_terms(0, kt, kML, pow2i(-e));
-        // P: 32 columns at a time, as packed pairs
-        float p_up = 1.f;
-        {
-          const float gr = tab_gh[row] + log2_scale, grl = tab_gl[row];
-          uint32_t u[32];
-          auto scores = [&](float down) {
-            float top = 0.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int cb = 2 * wg + c;               // columns 32 cb ..: zero above the diagonal
-              if (cb > w4) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) u[16 * c + i] = 0u;
-                continue;
-              }
-              float x[32];
-              tmem_ld32(tl + kColP + 32 * cb, x);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 h4 = *reinterpret_cast<const float4*>(tab_gh + 32 * cb + i);
-                float d[4] = {gr - h4.x, gr - h4.y, gr - h4.z, gr - h4.w};
-                if (big) {
-                  const float4 l4 = *reinterpret_cast<const float4*>(tab_gl + 32 * cb + i);
-                  // (the scale's logarithm joins the low parts: gr - h4 alone is exact where it matters)
-                  d[0] = (tab_gh[row] - h4.x) + ((grl - l4.x) + log2_scale);
-                  d[1] = (tab_gh[row] - h4.y) + ((grl - l4.y) + log2_scale);
-                  d[2] = (tab_gh[row] - h4.z) + ((grl - l4.z) + log2_scale);
-                  d[3] = (tab_gh[row] - h4.w) + ((grl - l4.w) + log2_scale);
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const float v = x[i + y] * ex2(d[y]);
-                  x[i + y] = (cb < w4 || i + y <= lane) && (!kF16 || row < L) ? v : 0.f;
-                  if constexpr (kF16) {
-                    top = fmaxf(top, fabsf(x[i + y]));
-                    x[i + y] *= down;
-                  }
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) u[16 * c + i] = Op16<T>::pack2(x[2 * i], x[2 * i + 1]);
-            }
-            return top;
-          };
-          const float top = scores(1.f);
-          if constexpr (kF16) {
-            if (!named_bar_and(1, kCompute, top < 32768.f)) {
-              const int pe = exponent_of(reduce_max(top)) - 14;
-              p_up = pow2i(pe);
-              scores(pow2i(-pe));
-            }
-          }
-          tmem_st16(tl + kColP + 64 * wg, u);
-          tmem_st16(tl + kColP + 64 * wg + 16, u + 16);
-          tmem_wait_st();
-          tc_fence_before();
-          arrive_warp(&bars[kPt]);
-        }
-        if (upd) {
-          wait(&bars[kMlFree], mn++ & 1);
-          make_terms(1, kt, kML, pow2i(-e));
-        }
+        const float up = make_scores(L);
         arrive_warp(&bars[kTabEmpty]);
-        if (upd) {
-          update_state(gam, pow2i(e));
-        }
-        wait(&bars[kOiDone], qn & 1);
-        if (upd && b + 1 < nb) write_copy();
-        // o, staged as [token][column] in kML
+        if (upd) update_state(gam, pow2i(-e));
         wait(&bars[kOFull], qn & 1);
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x[16], y[16];
-          tmem_ld16(tl + kColOi + 64 * wg + 16 * c, x);
-          tmem_ld16(tl + kColOa + 64 * wg + 16 * c, y);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = fmaf(row_gam, x[i], kF16 ? y[i] * p_up : y[i]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<uint4*>(sm + kML + wg * 16384 + row * 128 + (((2 * c + i) ^ (row & 7)) << 4)) =
-                pack8<T>(x + 8 * i);
-        }
-        tc_fence_before();
-        arrive_warp(&bars[kOFree]);
-        fence_async_smem();
-        named_bar_sync(1, kCompute);
-        if (L == kB) {
-          if (tid == 0) {
-            tma_store_3d(&om, sm + kML, 0, it.h, t);
-            if (p.dv > 64) tma_store_3d(&om, sm + kML + 16384, 64, it.h, t);
-            bulk_commit_group();
-          }
-        } else {
-          T* o = static_cast<T*>(p.o);
-          const int chunks = p.dv / 8;
-          for (int i = tid; i < L * chunks; i += kCompute) {
-            const int rr = i / chunks, c = i - rr * chunks;
-            __stcs(reinterpret_cast<uint4*>(o + ((size_t)(t + rr) * p.Hv + it.h) * p.dv + 8 * c),
-                   *reinterpret_cast<const uint4*>(sm + kML + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)));
-          }
-        }
+        write_o(t, it.h, L, row_gam, up);
+        if (upd && b + 1 < nb) write_copy();
       }
       if (last) {
-        // the state after the sequence; state_out may be state_in, whose reader is then the first segment
-        if (it.J > 1 && tid == 0)
-          wait.flag(reinterpret_cast<uint32_t*>(p.ws) + (it.first % G) * kFlagWords + kDone, it.first / G + 1);
-        acquire_stage();
+        // the state after the sequence
+        if (it.J > 1) wait(&bars[kOutOk], okn++ & 1);
+        if (lane == 0) bulk_wait_read_all();
+        sync();
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          *reinterpret_cast<float4*>(sm + kStage + (2 * wg + (c >> 3)) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-              make_float4(S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]);
+        for (int x = 0; x < 64; ++x) *staged(x) = S[x];
         fence_async_smem();
-        named_bar_sync(1, kCompute);
+        sync();
         if (tid == 0) {
           for (int x = 0; 32 * x < p.dk; ++x)
             tma_store_3d(&som, sm + kStage + x * 16384, 32 * x, 0, it.n * p.Hv + it.h);
@@ -875,7 +1028,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         }
       }
     }
-    if (tid == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
