@@ -371,18 +371,6 @@ gdn_status with_dk(int dk, F f) {
   }
 }
 
-// 3-D map over fp32 states [rows][dv][dk]: boxes of 32 columns and 128 rows of one state.
-bool make_state_map(CUtensorMap* m, const void* base, int dk, int dv, int64_t rows) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)dk, (cuuint64_t)dv, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)dk * 4, (cuuint64_t)dv * dk * 4};
-  cuuint32_t box[3] = {32, 128, 1}, estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr int kLinearCtas = 148;   // CTAs that the workspace is laid out for: one on each SM
 
 bool linear_on_tensor_cores(gdn_dtype dtype, int64_t total_T) { return dtype != GDN_F32 && total_T > 0; }
@@ -398,7 +386,7 @@ int linear_segment(int n_seqs, int64_t total_T, int Hv) {
 
 template <typename T>
 gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const void* v, int64_t total_T,
-                            const float* state_in, gdn::ltc::Params prm, CUtensorMapDataType ty, cudaStream_t st) {
+                            gdn::ltc::Params prm, CUtensorMapDataType ty, cudaStream_t st) {
   const int sms = sm_count();
   if (sms < 16) return fail(GDN_ERR_CUDA, "%s: cannot query the multiprocessor count", fn);
   const int64_t items = (total_T / (prm.seg * gdn::ltc::kB) + prm.n_seqs) * prm.Hv;   // at most
@@ -407,16 +395,14 @@ gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const 
   if (!prm.ws) prm.panel = prm.Hv;
   // about 2 s, and ten times what the blocks take (4000 cycles each)
   prm.limit = 4000000000ll + (total_T / gdn::ltc::kB + prm.n_seqs) * prm.Hv / grid * 40000;
-  const int64_t states = (int64_t)prm.n_seqs * prm.Hv;
-  CUtensorMap qm, km, vm, om, sim, som;
+  CUtensorMap qm, km, vm, om;
   if (!make_map(&qm, q, prm.dk, prm.Hqk, (int)total_T, 64, ty, gdn::ltc::kB) ||
       !make_map(&km, k, prm.dk, prm.Hqk, (int)total_T, 64, ty, gdn::ltc::kB) ||
       !make_map(&vm, v, prm.dv, prm.Hv, (int)total_T, 64, ty, gdn::ltc::kB) ||
-      !make_map(&om, prm.o, prm.dv, prm.Hv, (int)total_T, 64, ty, 32) ||
-      !make_state_map(&sim, state_in ? state_in : prm.state_out, prm.dk, prm.dv, states) ||
-      !make_state_map(&som, prm.state_out, prm.dk, prm.dv, states))
+      !make_map(&om, prm.o, prm.dv, prm.Hv, (int)total_T, 64, ty, 32))
     return fail(GDN_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable or failed", fn);
-  auto kern = gdn::ltc::prefill_kernel<T>;
+  auto kern = prm.dk == gdn::ltc::kD && prm.dv == gdn::ltc::kD ? gdn::ltc::prefill_kernel<T, true>
+                                                               : gdn::ltc::prefill_kernel<T, false>;
   if (gdn_status s = allow_smem(kern, fn)) return s;
   if (prm.ws) {
     cudaError_t e = cudaMemsetAsync(prm.ws, 0, gdn::ltc::Workspace::flags_bytes(grid), st);
@@ -432,7 +418,7 @@ gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const 
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = prm.ws ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qm, km, vm, om, sim, som, prm);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qm, km, vm, om, prm);
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return launch_status(fn);
 }
@@ -567,8 +553,8 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
     prm.scale = scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == GDN_F16)
-      return launch_linear_tc<__half>(fn, q, k, v, total_T, state_in, prm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, st);
-    return launch_linear_tc<__nv_bfloat16>(fn, q, k, v, total_T, state_in, prm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, st);
+      return launch_linear_tc<__half>(fn, q, k, v, total_T, prm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, st);
+    return launch_linear_tc<__nv_bfloat16>(fn, q, k, v, total_T, prm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, st);
   }
   return with_dtype(dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;

@@ -8,12 +8,18 @@
 //   P_rs = scale exp(G_r - G_s) q_r . k_s  (s <= r),   o_r = exp(G_r) scale S q_r + sum_s P_rs v_s
 //   S   <- exp(G_L) S + sum_s v_s (exp(G_L - G_s) k_s)^T
 //
-// Four products a block, each 128 x 128 x 128: Q K^T, Q S^T, P V and K~^T V with
+// o is computed as rho_r (q_r S + sum_s P'_rs v_s), rho_r = scale exp(G_r), P'_rs =
+// exp(-G_s) q_r . k_s, so that both products go to one accumulator and a score's weight
+// depends on its column alone. That is exact while exp(-G_s) stays in range; a steep block
+// (2^60 or more; f16 2^20) takes a power of two 2^-m_r out of its late rows, from P' by the exponent
+// and from q_r, after Q K^T, exactly.
+//
+// Four products a block, each 128 x 128 x 128: Q K^T, Q S^T, P' V and K~^T V with
 // K~_s = w_s k_s, w_s = exp(G_L - G_s). The state lives, transposed, in fp32 registers
 // of the compute warps (64 values a thread); the tensor core reads a rounded copy of it,
 // for o alone.
 //
-// Precision. o has 16 bits, so P and the copy of S that Q meets are rounded to the
+// Precision. o has 16 bits, so P' and the copy of S that Q meets are rounded to the
 // input type (half a step each, and no term of o carries both). The state is fp32, so
 // K~ is not rounded but split into terms that are multiplied with V one after another
 // into one accumulator. With w = w1 + w2 + w3 (each of the input type's precision)
@@ -24,13 +30,11 @@
 // 24 bits in bf16. f16 needs hi and rn(w2 k + e1), 22 bits; in bf16 the same two (16
 // bits) serve where the state is only read for o, inside a segment that is not a
 // sequence's last. In f16 powers of two keep what is rounded in the type's range: one
-// from the block's largest |k| and w for the terms of K~, one from the largest |S| for
-// the copy of S, and one for P where a score passes 2^15.
+// from the block's largest |k| and w for the terms of K~, and one from the largest |S| and
+// |P'| for the copy of S and P', which share an accumulator.
 // Log-decays are summed in fp64 (exp(G_r - G_s) of far tokens is a difference of large
 // sums) and clamped where exp is zero in fp32, so that a reset (-inf) does not turn
-// differences into NaN. For tokens r, s of different quarters of the block the weight of
-// P is the product of a factor of r and one of s, around the end of s's quarter; inside
-// a quarter it is exp(G_r - G_s) itself.
+// differences into NaN.
 //
 // What bounds it. The data move once through HBM at 128 KB a block (fewer where heads
 // share k and q); the products' operands pass shared memory (128 bytes a cycle), which
@@ -56,7 +60,8 @@
 // Roles. Warps 0-7 compute. Warp 8 walks the items, hands them to the others through a
 // ring and loads K, V; warp 9 issues the products; warp 10 loads Q and computes the
 // decay tables; warp 11, the courier, waits for and sets the flags in global memory, so
-// that the compute warps wait for none of those; warps 12-15 scan.
+// that the compute warps wait for none of those; warps 12-15 scan. Sixteen compute warps
+// with half the columns each were slower (560 against 456 us on eight packed sequences).
 //
 // Order and progress. Items are numbered (sequence, panel, segment, head). Every
 // wait on another CTA is for work of a lower number -- B(i) and scan(i) for scans
@@ -79,60 +84,74 @@ using namespace sm100;
 
 constexpr int kB = 128;              // tokens per block
 constexpr int kD = 128;              // padded head size
-constexpr int kCompute = 256;        // warps 0-7
+constexpr int kComputeWarps = 8;     // warps 0-7
+constexpr int kCompute = 32 * kComputeWarps;
 constexpr int kLoadWarp = 8;         // items; K, V tiles
 constexpr int kMmaWarp = 9;          // tensor-core work
 constexpr int kGateWarp = 10;        // Q tiles and the decay tables
 constexpr int kCourierWarp = 11;     // flags in global memory
 constexpr int kScanWarp = 12;        // to 15
 constexpr int kScanWarps = 4;
-constexpr int kThreads = 32 * (kScanWarp + kScanWarps);
+constexpr int kWarps = kScanWarp + kScanWarps;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kSlices = 32;          // owners of one head's state
-// Registers: 512 threads start with 128 each; the compute warps' share grows by what
-// the others give back (256 x 176 + 256 x 80 = 65536, all that the block holds).
+// Registers: 512 threads start with 128 each; the compute warps' share grows by what the
+// others give back (256 x 176 + 256 x 80 = 65536, all that the block holds).
 constexpr int kRegsCompute = 176, kRegsOther = 80;
-static_assert(kCompute * kRegsCompute + (kThreads - kCompute) * kRegsOther <= 65536, "register file");
+static_assert(kCompute * kRegsCompute + (kThreads - kCompute) * kRegsOther <= kThreads * 128, "register file");
 constexpr int kStateBytes = kD * kD * 4;
 constexpr float kMinLog = -105.f;  // exp is 0 in fp32, subnormals included
 
+// A block is steep when its log-decay (base 2) reaches this. In f16 P' has to fit beside the
+// other rows' and the copy of S: 20 bits leave the smallest rows 20 bits below their largest.
+template <typename T> constexpr int kSteep = std::is_same<T, __half>::value ? 20 : 60;
+
 // ---- shared memory (bytes) ----
-constexpr uint32_t kQ = 0;                     // [128][128] as two K-major 128B-swizzled atoms, 16 KB apart
-constexpr uint32_t kK = 32768;                 // two buffers
-constexpr uint32_t kV = 98304;                 // two buffers
-constexpr uint32_t kS = 163840;                // the rounded copy of S, [d_k][d_v] as two MN-major atoms
-constexpr uint32_t kO = 196608;                // o on its way out
-constexpr uint32_t kStage = kS;                // kS and kO together: a state on its way in or out
+constexpr uint32_t kQ = 0;                     // two buffers of [128][128], two K-major 128B-swizzled atoms 16 KB apart;
+                                               // o goes out through the buffer that its Q came in
+constexpr uint32_t kK = 65536;                 // two buffers
+constexpr uint32_t kV = 131072;                // two buffers
+constexpr uint32_t kS = 196608;                // the rounded copy of S, [d_k][d_v] as two MN-major atoms
 constexpr uint32_t kTab = 229376;              // w (bf16: words wp1[64], wp2[64], wp3[64]; f16: float[128]), then
 constexpr uint32_t kTabGam = kTab + 768;       // float gam[128], gp[128], gb[128]
 constexpr uint32_t kBars = kTabGam + 1536;
-constexpr uint32_t kRing = kBars + 256;        // items
+constexpr uint32_t kRing = kBars + 320;        // items
 constexpr uint32_t kMisc = kRing + 192;        // words: see Misc
-constexpr uint32_t kSmem = kMisc + 256;
+constexpr uint32_t kSmem = kMisc + 192;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 constexpr int kRingItems = 4;
 
-enum Bar { kKvFull = 0, kKvEmpty = 2, kItFull = 4, kItEmpty = 8, kQFull = 12, kTabFull, kTabEmpty, kPFull, kKt, kPt, kUFull,
-           kOFull, kStFull, kSlotFree, kPub, kInReady, kGot, kOutOk, kCBar, kNumBars };
-static_assert(kNumBars * 8 <= 256, "barriers");
+// A barrier's waiters go by the parity of its phase, so none may complete a second phase
+// before all of them have seen the first: each next completion has to need something that
+// they do after that wait. Hence two barriers for pass A's two accumulators (kUFull,
+// kURead) and four, as many as there are ring items, for kGot: the courier may fall behind
+// the compute warps by that many and hands its item back after it.
+enum Bar { kKvFull = 0, kKvEmpty = 2, kItFull = 4, kItEmpty = 8, kGot = 12, kUFull = 16, kURead = 18, kKt = 20, kHalf = 22,
+           kQFull = 24, kQFree = 26, kTabEmpty = 28, kPFull, kSReady, kOFull, kSlotFree, kPub, kInReady, kOutOk, kCBar,
+           kLeft, kNumBars };
+static_assert(kNumBars * 8 <= 320, "barriers");
 
 struct Misc {
   uint32_t tmem;
+  uint32_t dead;       // a wait ran out
   float gam_l;         // exp(G_L) of the block
   float seg_gam;       // exp of the segment's total log-decay, up to this block
   float w_max;         // the largest w of the block
-  float tot[4];        // the quarters' total log-decays (base 2)
-  float red[2][8];     // reductions over the compute warps (f16)
+  uint32_t steep;      // exp(-G) reaches 2^kSteep in the block
+  int start_i[4];      // the log-decays (base 2) up to each quarter: whole part
+  float start_f[4];    // and the rest
+  float red[2][kComputeWarps];   // reductions over the compute warps (f16)
 };
-static_assert(sizeof(Misc) <= 256, "shared memory budget");
+static_assert(sizeof(Misc) <= 192, "shared memory budget");
 
 // ---- tensor memory columns ----
-// The terms of K~ lie where Q S^T and P V go later in the block: each K half (tokens
-// 0-63, 64-127) in the 64 columns that the warps which write it also read o from.
-constexpr uint32_t kColP = 0;        // Q K^T, then P in place (16 bits: columns 0-31 and 64-95)
-constexpr uint32_t kColOi = 128;     // t4, h2; then Q S^T
-constexpr uint32_t kColOa = 256;     // hi, e1 (or the second of two terms); then P V
-constexpr uint32_t kColU = 384;      // K~^T V
-constexpr uint32_t kColHi = kColOa, kColE1 = kColOa + 32, kColT4 = kColOi, kColH2 = kColOi + 32;
+// Each of two terms of K~ has 32 columns for either half of the tokens (0-63, 64-127);
+// pass A's other two lie where o goes in pass B. P', packed, takes the first half of either
+// 64 columns of Q K^T.
+constexpr uint32_t kColP = 0;        // Q K^T, then P' in place
+constexpr uint32_t kColO = 128;      // Q S^T + P' V
+constexpr uint32_t kColK = 256;      // terms of K~
+constexpr uint32_t kColU = 384;      // K~^T V (pass A: every other block's over P)
 
 // ---- workspace ----
 constexpr int kFlagWords = 32;       // per CTA: out_ready[2], scanned[2], in_cnt[2], done
@@ -157,19 +176,37 @@ struct Params {
   long long limit;     // SM cycles that a wait lasts at most
 };
 
-// Waits that stop waiting once one has run out. The limit grows with the problem: a
-// scan warp may wait for a sequence that comes at the end.
+// Waits give up once `dead` is set, and the roles leave their loops; the kernel's end
+// reports it. Waits for a flag in global memory set it when their time is over, and for
+// those on chip the watchdog (the last warp, once its scan is done) does when the kernel's is:
+// so the wait itself, of which there are many, is five instructions long. The limit grows
+// with the problem: a scan warp may wait for a sequence that comes at the end.
 struct Wait {
+  uint32_t dead;       // shared-memory address
   long long limit;
-  bool ok = true;
-  __device__ __forceinline__ explicit Wait(long long l) : limit(l) {}
-  // by the whole warp, which agrees on the outcome
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, limit));
+  __device__ __forceinline__ bool ok() const {
+    uint32_t d;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
+    return d == 0;
   }
-  // by one lane
-  __device__ __forceinline__ void flag(const uint32_t* p, uint32_t target) {
-    if (ok) ok = wait_flag_geq(p, target, limit);
+  __device__ __forceinline__ void give_up() const {
+    asm volatile("st.volatile.shared.b32 [%0], 1;" ::"r"(dead) : "memory");
+  }
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 d;\n\t"
+        "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+        "@p bra D%=;\n\t"
+        "ld.volatile.shared.b32 d, [%2];\n\t"
+        "setp.eq.u32 q, d, 0;\n\t"
+        "@q bra W%=;\n\t"
+        "D%=:\n\t}" ::"r"(smem_u32(bar)),
+        "r"(parity), "r"(dead)
+        : "memory");
+  }
+  // on a flag in global memory, by one lane
+  __device__ __forceinline__ void flag(const uint32_t* p, uint32_t target) const {
+    if (ok() && !wait_flag_geq(p, target, limit)) give_up();
   }
 };
 
@@ -280,8 +317,47 @@ template <> struct Two<__half> {
     return d;
   }
 };
+// Twice 32 columns of 32 lanes, waited for together.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t tb, float* x, float* y) {
+  uint32_t u[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]), "=r"(u[32]),
+        "=r"(u[33]), "=r"(u[34]), "=r"(u[35]), "=r"(u[36]), "=r"(u[37]), "=r"(u[38]), "=r"(u[39]), "=r"(u[40]),
+        "=r"(u[41]), "=r"(u[42]), "=r"(u[43]), "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]), "=r"(u[48]),
+        "=r"(u[49]), "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]), "=r"(u[56]),
+        "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]), "=r"(u[62]), "=r"(u[63])
+      : "r"(ta), "r"(tb)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    x[i] = __uint_as_float(u[i]);
+    y[i] = __uint_as_float(u[32 + i]);
+  }
+}
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+__device__ __forceinline__ void st_relaxed_gpu(uint32_t* p, uint32_t v) {
+  asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_add_relaxed_gpu(uint32_t* p, uint32_t v) {
+  asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t neg2(uint32_t a) { return a ^ 0x80008000u; }
 
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t u) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(u) : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four K-steps with A in TMEM (8 columns a step) and B advancing BSTEP 16-byte units a
@@ -317,6 +393,14 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // The exponent e with |x| < 2^(e + 1) (x finite; 128 for infinities and NaN).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
+// A value that the compiler does not take for a loop's invariant: it would write the loop
+// out once for each outcome of a condition on it, and the instruction cache is small.
+__device__ __forceinline__ bool each_time(bool x) {
+  uint32_t y = x;
+  asm volatile("" : "+r"(y));
+  return y != 0;
+}
+
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -330,7 +414,6 @@ __device__ __forceinline__ void scan_role(const Params& p, int ow, int G) {
   uint32_t* flags = reinterpret_cast<uint32_t*>(p.ws);
   const float* meta = reinterpret_cast<const float*>(p.ws + Workspace::meta_offset(G));
   uint8_t* slots = p.ws + Workspace::slots_offset(G);
-  Wait wait(p.limit);
   int base = 0;
   for (int n0 = 0; n0 < p.n_seqs; n0 += 32) {
     int J = 0;
@@ -349,40 +432,72 @@ __device__ __forceinline__ void scan_role(const Params& p, int ow, int G) {
           // word x = v * 256 + t of a slot holds rows (d_v) 64 (t / 128) + 4 v .. + 3 of column t % 128
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int t = 128 * (sl & 1) + 32 * u + lane, col = t & 127, row = 64 * (t >> 7) + 4 * (sl >> 1);
+            const int col = 32 * u + lane, row = 64 * (sl & 1) + 4 * (sl >> 1);
             S[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (p.state_in && row < p.dv && col < p.dk) {   // (d_v is a multiple of 4)
               const float* x = p.state_in + (((size_t)(n0 + i) * p.Hv + h0 + hl) * p.dv + row) * p.dk + col;
               S[u] = make_float4(__ldcg(x), __ldcg(x + p.dk), __ldcg(x + 2 * p.dk), __ldcg(x + 3 * p.dk));
             }
           }
-          for (int j = 0; j + 1 < Jn; ++j) {
-            const int item = base + h0 * Jn + j * hp + hl, c = item % G, r = item / G;
-            const int dst = item + hp, c2 = dst % G, r2 = dst / G;
-            if (lane == 0) wait.flag(flags + c * kFlagWords + kOutReady + (r & 1), r + 1);
-            __syncwarp();
-            const float gam = __ldcg(meta + 2 * c + (r & 1));
-            const float4* src = reinterpret_cast<const float4*>(slots + (size_t)(4 * c + (r & 1)) * kStateBytes) + 128 * sl;
-            float4 L[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) L[u] = __ldcg(src + 32 * u + lane);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              S[u].x = fmaf(gam, S[u].x, L[u].x);
-              S[u].y = fmaf(gam, S[u].y, L[u].y);
-              S[u].z = fmaf(gam, S[u].z, L[u].z);
-              S[u].w = fmaf(gam, S[u].w, L[u].w);
+          long long t0 = 0;
+          for (int j = 0; j + 1 < Jn;) {
+            // One look at the flags of up to two segments: lanes 0 and 1 whether segments j
+            // and j + 1 are published, lanes 2 and 3 whether the slots that their results go
+            // to have been read.
+            const int jl = j + (lane & 1), item = base + h0 * Jn + jl * hp + hl;
+            const int at = lane < 2 ? item : item + hp, c = at % G, r = at / G;
+            const uint32_t need = lane < 2 ? r + 1 : max(r - 1, 0);
+            bool ready = false;
+            if (lane < 4 && jl + 1 < Jn)
+              ready = ld_acquire_gpu(flags + c * kFlagWords + (lane < 2 ? kOutReady + (r & 1) : kDone)) >= need;
+            const uint32_t bits = __ballot_sync(0xffffffffu, ready);
+            const int m = (bits & 5u) != 5u ? 0 : (bits & 10u) != 10u ? 1 : 2;
+            if (m == 0) {
+              const long long now = clock64();
+              if (t0 == 0) t0 = now;
+              if (__any_sync(0xffffffffu, now - t0 > p.limit)) {
+                if (lane == 0) flag_error(kErrTimeout);
+                return;
+              }
+              __nanosleep(20);
+              continue;
             }
-            if (lane == 0 && r2 >= 2) wait.flag(flags + c2 * kFlagWords + kDone, r2 - 1);
-            __syncwarp();
-            float4* d = reinterpret_cast<float4*>(slots + (size_t)(4 * c2 + 2 + (r2 & 1)) * kStateBytes) + 128 * sl;
+            t0 = 0;
+            float4 L[2][4];
+            float gam[2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) __stcg(d + 32 * u + lane, S[u]);
-            __syncwarp();
-            if (lane == 0) {
-              red_add_release_gpu(flags + c2 * kFlagWords + kInCnt + (r2 & 1), 1u);
-              red_add_release_gpu(flags + c * kFlagWords + kScanned + (r & 1), 1u);
+            for (int x = 0; x < 2; ++x) {
+              if (x < m) {
+                const int src = item - (lane & 1) * hp + x * hp, cs = src % G, rs = src / G;
+                gam[x] = __ldcg(meta + 2 * cs + (rs & 1));
+                const float4* from =
+                    reinterpret_cast<const float4*>(slots + (size_t)(4 * cs + (rs & 1)) * kStateBytes) + 128 * sl;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) L[x][u] = __ldcg(from + 32 * u + lane);
+              }
             }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x < m) {
+                const int dst = item - (lane & 1) * hp + (x + 1) * hp, cd = dst % G, rd = dst / G;
+                float4* to = reinterpret_cast<float4*>(slots + (size_t)(4 * cd + 2 + (rd & 1)) * kStateBytes) + 128 * sl;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  S[u].x = fmaf(gam[x], S[u].x, L[x][u].x);
+                  S[u].y = fmaf(gam[x], S[u].y, L[x][u].y);
+                  S[u].z = fmaf(gam[x], S[u].z, L[x][u].z);
+                  S[u].w = fmaf(gam[x], S[u].w, L[x][u].w);
+                  __stcg(to + 32 * u + lane, S[u]);
+                }
+              }
+            }
+            __syncwarp();
+            // lanes 0 (and 1): the published slot is free; 2 (and 3): the entering state is there
+            if (lane < 4 && (lane & 1) < m) {
+              fence_acq_rel_gpu();
+              red_add_relaxed_gpu(flags + c * kFlagWords + (lane < 2 ? kScanned : kInCnt) + (r & 1), 1u);
+            }
+            j += m;
           }
         }
       }
@@ -398,11 +513,11 @@ __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
 }
 
-template <typename T>
+// kWhole: d_k = d_v = 128.
+template <typename T, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
-               const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap om,
-               const __grid_constant__ CUtensorMap sim, const __grid_constant__ CUtensorMap som, const Params p) {
+               const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap om, const Params p) {
   constexpr bool kF16 = std::is_same<T, __half>::value;
   constexpr uint32_t kFmt = Op16<T>::kFmt;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -411,9 +526,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   Item* ring = reinterpret_cast<Item*>(sm + kRing);
   uint32_t* tab_wp = reinterpret_cast<uint32_t*>(sm + kTab);    // bf16: three words of pairs
   float* tab_w = reinterpret_cast<float*>(sm + kTab);           // f16
-  float* tab_gam = reinterpret_cast<float*>(sm + kTabGam);      // exp(G_r) scale
-  float* tab_gp = tab_gam + kB;                                 // log2 decay from the start of r's quarter to r
-  float* tab_gb = tab_gam + 2 * kB;                             // exp of the decay from s to the end of its quarter
+  float* tab_gam = reinterpret_cast<float*>(sm + kTabGam);      // rho_r = exp(G_r) scale
+  float* tab_gp = tab_gam + kB;       // minus the log-decay (base 2) from the start of s's quarter to s
+  float* tab_gb = tab_gam + 2 * kB;   // exp(-G_s)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = gridDim.x, cta = blockIdx.x;
 
@@ -423,11 +538,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   }
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool warps = i == kTabEmpty || i == kKt || i == kPt || i == kPub || i == kGot || i == kCBar;
-      const bool readers = i >= kItEmpty && i < kItEmpty + kRingItems;
-      mbar_init(&bars[i], warps ? 8 : readers ? (p.ws ? 11 : 10) : 1);
+      const bool warps = (i >= kGot && i < kGot + 4) || i == kURead || i == kURead + 1 || i == kQFree || i == kQFree + 1 ||
+                         i == kTabEmpty || i == kSReady || i == kPub || i == kCBar;
+      const bool readers = i >= kItEmpty && i < kItEmpty + kRingItems, both = i == kKvFull || i == kKvFull + 1;
+      mbar_init(&bars[i], warps ? kComputeWarps : i == kKt || i == kKt + 1 ? kComputeWarps / 2
+                          : readers ? kComputeWarps + (p.ws ? 3 : 2) : i == kLeft ? kWarps - 1 : both ? 2 : 1);
     }
     fence_mbar_init();
+    misc->dead = 0;
   }
   if (warp == 0) {
     tmem_alloc(&misc->tmem, 512);
@@ -438,13 +556,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = misc->tmem;
   const uint32_t sbase = smem_u32(sm);
-  Wait wait(p.limit);
+  const Wait wait{smem_u32(&misc->dead), p.limit};
   // the CTA's i-th item, false behind the last
   auto next_item = [&](uint32_t i, Item& it) {
     wait(&bars[kItFull + (i & 3)], (i >> 2) & 1);
-    if (!wait.ok) return false;
+    if (!wait.ok()) return false;
     it = ring[i & 3];
-    arrive_warp(&bars[kItEmpty + (i & 3)]);
+    if (warp != kCourierWarp) arrive_warp(&bars[kItEmpty + (i & 3)]);
     return it.n >= 0;
   };
   Item it;
@@ -452,11 +570,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   if (warp == kLoadWarp) {
     give_registers();
     // ------------------------------------------------- items; K, V tiles ---
-    const uint64_t once = l2_evict_first_policy();
+    const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
     Walk walk;
     uint32_t cnt = 0;
     bool more = true;
-    for (uint32_t i = 0; more && wait.ok; ++i) {
+    for (uint32_t i = 0; more && wait.ok(); ++i) {
       more = walk.find(p, cta + (int)i * G, it);
       if (!more) it.n = -1;
       if (i >= kRingItems) wait(&bars[kItEmpty + (i & 3)], ((i >> 2) - 1) & 1);
@@ -465,166 +583,211 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       if (!more) break;
       const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
       const bool shared_k = p.Hv != p.Hqk;
+#pragma unroll 1
       for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
+#pragma unroll 1
         for (int b = 0; b < nb; ++b, ++cnt) {
           const uint32_t s = cnt & 1;
           if (cnt >= 2) wait(&bars[kKvEmpty + s], ((cnt >> 1) - 1) & 1);
-          if (!wait.ok) break;
+          if (!wait.ok()) break;
           const int t = it.t0 + b * kB;
           uint64_t* full = &bars[kKvFull + s];
           mbar_arrive_expect_tx_warp(full, 65536);
           uint8_t *kt = sm + kK + s * 32768, *vt = sm + kV + s * 32768;
           // the second pass is the last to read V, and K where no other head shares it
-          if (pass == 0 || shared_k) {
-            tma_load_3d_warp(kt, &km, full, 0, hq, t);
-            tma_load_3d_warp(kt + 16384, &km, full, 64, hq, t);
-          } else {
-            tma_load_3d_warp_hint(kt, &km, full, 0, hq, t, once);
-            tma_load_3d_warp_hint(kt + 16384, &km, full, 64, hq, t, once);
-          }
-          if (pass == 0) {
-            tma_load_3d_warp(vt, &vm, full, 0, it.h, t);
-            tma_load_3d_warp(vt + 16384, &vm, full, 64, it.h, t);
-          } else {
-            tma_load_3d_warp_hint(vt, &vm, full, 0, it.h, t, once);
-            tma_load_3d_warp_hint(vt + 16384, &vm, full, 64, it.h, t, once);
-          }
+          const uint64_t pv = pass == 0 ? again : once, pk = pass == 0 || shared_k ? again : once;
+          tma_load_3d_warp_hint(kt, &km, full, 0, hq, t, pk);
+          tma_load_3d_warp_hint(kt + 16384, &km, full, 64, hq, t, pk);
+          tma_load_3d_warp_hint(vt, &vm, full, 0, it.h, t, pv);
+          tma_load_3d_warp_hint(vt + 16384, &vm, full, 64, it.h, t, pv);
         }
       }
     }
     // tiles still on their way land before the CTA ends
-    for (uint32_t c = cnt >= 2 ? cnt - 2 : 0; c < cnt; ++c) mbar_wait(&bars[kKvFull + (c & 1)], (c >> 1) & 1, p.limit);
+    for (uint32_t c = cnt >= 2 ? cnt - 2 : 0; c < cnt; ++c) mbar_wait(&bars[kKvFull + (c & 1)], (c >> 1) & 1);
   } else if (warp == kGateWarp) {
     give_registers();
     // ------------------------------------------- Q tiles and decay tables ---
-    uint32_t qn = 0, tn = 0;
+    const uint64_t pol = p.Hv != p.Hqk ? l2_evict_normal_policy() : l2_evict_first_policy();
+    uint32_t qn = 0, cnt = 0;
+#pragma unroll 1
     for (uint32_t i = 0; next_item(i, it); ++i) {
       const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
+      const float* gh = p.g + it.h;
+#pragma unroll 1
       for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
         double seg = 0.0;
-        for (int b = 0; b < nb && wait.ok; ++b) {
-          const int t = it.t0 + b * kB, L = min(kB, it.len - b * kB);
-          float x[4];
+        float g[4];
+        // a block's log-decays, four consecutive tokens to a lane, fetched a block ahead
+        auto fetch = [&](int b) {
+          const int r = b * kB + 4 * lane;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int s = 4 * lane + e;
-            const float gv = s < L ? p.g[(size_t)(t + s) * p.g_stride + it.h] : 0.f;
-            x[e] = gv < kMinLog ? kMinLog : gv;
-          }
-          if (pass == 1) {
-            if (qn > 0) wait(&bars[kOFull], (qn - 1) & 1);
-            if (wait.ok) {
-              mbar_arrive_expect_tx_warp(&bars[kQFull], 32768);
-              tma_load_3d_warp(sm + kQ, &qm, &bars[kQFull], 0, hq, t);
-              tma_load_3d_warp(sm + kQ + 16384, &qm, &bars[kQFull], 64, hq, t);
-              ++qn;
-            }
-          }
+          for (int x = 0; x < 4; ++x)
+            g[x] = r + x < it.len ? gh[(size_t)(it.t0 + r + x) * p.g_stride] : 0.f;
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int b = 0; b < nb && wait.ok(); ++b, ++cnt) {
+          const int L = min(kB, it.len - b * kB);
+          // G, the log-decays (base 2) from the block's start, in fp64; rounded to fp32 as
+          // differences only
+          constexpr double kLog2E = 1.4426950408889634;
           double c[4];
-          c[0] = x[0]; c[1] = c[0] + x[1]; c[2] = c[1] + x[2]; c[3] = c[2] + x[3];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            c[x] = (g[x] < kMinLog ? kMinLog : g[x]) * kLog2E;
+            if (x > 0) c[x] += c[x - 1];
+          }
           double incl = c[3];
+          fetch(b + 1);
 #pragma unroll
           for (int off = 1; off < 32; off <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += y;
           }
-          const double end = __shfl_sync(0xffffffffu, incl, 31), before = incl - c[3];
-          const double q0 = __shfl_sync(0xffffffffu, before, lane & 24), q1 = __shfl_sync(0xffffffffu, incl, lane | 7);
-          seg += end;
-          float w[4], gm[4], gp[4], gb[4];
+          const double sum = __shfl_sync(0xffffffffu, incl, 31), before = incl - c[3];
+          const double start = __shfl_sync(0xffffffffu, before, lane & 24), whole = floor(start);
+          seg += sum;
+          float w[4], wm = 0.f;
+          float4 gam, gb, gp;
+          float *const gamx = &gam.x, *const gbx = &gb.x, *const gpx = &gp.x;
+          bool flat = true;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const double Gs = before + c[e];
-            w[e] = 4 * lane + e < L ? expf((float)(end - Gs)) : 0.f;
-            gm[e] = expf((float)Gs) * p.scale;
-            gp[e] = (float)((Gs - q0) * 1.4426950408889634);
-            gb[e] = expf((float)(q1 - Gs));
+          for (int x = 0; x < 4; ++x) {
+            const double G = before + c[x];
+            w[x] = 4 * lane + x < L ? ex2((float)(sum - G)) : 0.f;
+            gamx[x] = ex2((float)G) * p.scale;
+            gbx[x] = ex2((float)-G);
+            gpx[x] = (float)(start - G);
+            flat = flat && G > -kSteep<T>;
+            wm = fmaxf(wm, w[x]);
           }
-          float wm = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+          uint2 wp[3];
           if constexpr (kF16) {
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
+          } else {
+            float v[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              wp[term] = make_uint2(Op16<T>::pack2(v[0], v[1]), Op16<T>::pack2(v[2], v[3]));
+              const float2 lo = Op16<T>::unpack2(wp[term].x), hi = Op16<T>::unpack2(wp[term].y);
+              v[0] -= lo.x; v[1] -= lo.y; v[2] -= hi.x; v[3] -= hi.y;
+            }
           }
-          if (tn > 0) wait(&bars[kTabEmpty], (tn - 1) & 1);
+          const uint32_t steep = __any_sync(0xffffffffu, !flat);
+          const float gam_l = ex2((float)sum), seg_gam = ex2((float)seg), rest = (float)(start - whole);
+          const int whole_i = (int)whole;
+          // everything is ready before the tables may be written: they are one block's
+          if (cnt > 0) wait(&bars[kTabEmpty], (cnt - 1) & 1);
           if constexpr (kF16) {
             reinterpret_cast<float4*>(tab_w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
           } else {
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              const uint32_t lo = Op16<T>::pack2(w[0], w[1]), hi = Op16<T>::pack2(w[2], w[3]);
-              reinterpret_cast<uint2*>(tab_wp + 64 * term)[lane] = make_uint2(lo, hi);
-              const float2 a = Op16<T>::unpack2(lo), d = Op16<T>::unpack2(hi);
-              w[0] -= a.x; w[1] -= a.y; w[2] -= d.x; w[3] -= d.y;
-            }
+            for (int term = 0; term < 3; ++term) reinterpret_cast<uint2*>(tab_wp + 64 * term)[lane] = wp[term];
           }
-          reinterpret_cast<float4*>(tab_gam)[lane] = make_float4(gm[0], gm[1], gm[2], gm[3]);
-          reinterpret_cast<float4*>(tab_gp)[lane] = make_float4(gp[0], gp[1], gp[2], gp[3]);
-          reinterpret_cast<float4*>(tab_gb)[lane] = make_float4(gb[0], gb[1], gb[2], gb[3]);
-          if ((lane & 7) == 0) misc->tot[lane >> 3] = (float)((q1 - q0) * 1.4426950408889634);
+          reinterpret_cast<float4*>(tab_gam)[lane] = gam;
+          reinterpret_cast<float4*>(tab_gp)[lane] = gp;
+          reinterpret_cast<float4*>(tab_gb)[lane] = gb;
+          if ((lane & 7) == 0) {
+            misc->start_i[lane >> 3] = whole_i;
+            misc->start_f[lane >> 3] = rest;
+          }
           if (lane == 0) {
             misc->w_max = wm;
-            misc->gam_l = expf((float)end);
-            misc->seg_gam = expf((float)seg);
+            misc->steep = steep;
+            misc->gam_l = gam_l;
+            misc->seg_gam = seg_gam;
           }
-          arrive_warp(&bars[kTabFull]);
-          ++tn;
+          arrive_warp(&bars[kKvFull + (cnt & 1)]);   // (the block is there when K, V and these are)
+          if (pass == 1) {
+            const uint32_t q = qn & 1;
+            if (qn >= 2) wait(&bars[kQFree + q], ((qn >> 1) - 1) & 1);
+            if (wait.ok()) {
+              mbar_arrive_expect_tx_warp(&bars[kQFull + q], 32768);
+              tma_load_3d_warp_hint(sm + kQ + q * 32768, &qm, &bars[kQFull + q], 0, hq, it.t0 + b * kB, pol);
+              tma_load_3d_warp_hint(sm + kQ + q * 32768 + 16384, &qm, &bars[kQFull + q], 64, hq, it.t0 + b * kB, pol);
+              ++qn;
+            }
+          }
         }
       }
     }
-    if (qn > 0) mbar_wait(&bars[kQFull], (qn - 1) & 1, p.limit);
+    for (uint32_t q = qn >= 2 ? qn - 2 : 0; q < qn; ++q) mbar_wait(&bars[kQFull + (q & 1)], (q >> 1) & 1);
   } else if (warp == kMmaWarp) {
     give_registers();
     // ------------------------------------------------- tensor-core work ---
     constexpr uint32_t id_qk = idesc_f16kind(128, 128, false, false, kFmt);   // both K-major
     constexpr uint32_t id_mn = idesc_f16kind(128, 128, false, true, kFmt);    // B MN-major
-    uint32_t cnt = 0, qn = 0, un = 0;
+    // (one copy of each product's code: the loops of all roles share the instruction cache)
+    uint32_t cnt = 0, qn = 0, tn = 0, un0 = 0, un1 = 0;   // tn: K~s; un: uses of either accumulator
+#pragma unroll 1
     for (uint32_t i = 0; next_item(i, it); ++i) {
       const int nb = (it.len + kB - 1) / kB;
       const bool last = it.j + 1 == it.J;
+#pragma unroll 1
       for (int pass = last ? 1 : 0; pass < 2; ++pass) {
-        for (int b = 0; b < nb && wait.ok; ++b, ++cnt) {
+        const bool a = pass == 0;
+#pragma unroll 1
+        for (int b = 0; b < nb && wait.ok(); ++b, ++cnt) {
+          const bool a = each_time(pass == 0);
           const uint32_t s = cnt & 1;
-          const uint32_t kt = sbase + kK + s * 32768;
           const uint64_t vd = desc_mnmajor(sbase + kV + s * 32768, 0, 128, 16384);
-          const uint64_t vd4 = desc_advance(vd, 4 * 2048);
-          const bool upd = pass == 0 || last || b + 1 < nb;   // the state after the segment comes from pass A
-          const bool four = !kF16 && (pass == 0 || last);
+          const uint64_t qd = desc_kmajor(sbase + kQ + (qn & 1) * 32768, 0, 16384);
           wait(&bars[kKvFull + s], (cnt >> 1) & 1);
-          if (pass == 1) {
-            wait(&bars[kQFull], qn & 1);
+          if (!a) {
+            wait(&bars[kQFull + (qn & 1)], (qn >> 1) & 1);
             tc_fence_after();
-            const uint64_t qd = desc_kmajor(sbase + kQ, 0, 16384), kd = desc_kmajor(kt, 0, 16384);
-            mma_run_warp<4, 2, 2>(tmem + kColP, qd, kd, id_qk, 0);
-            mma_run_warp<4, 2, 2>(tmem + kColP, desc_advance(qd, 16384), desc_advance(kd, 16384), id_qk, 1);
+            const uint64_t kd = desc_kmajor(sbase + kK + s * 32768, 0, 16384);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              mma_run_warp<4, 2, 2>(tmem + kColP, desc_advance(qd, 16384 * h), desc_advance(kd, 16384 * h), id_qk, h);
             mma_commit_warp(&bars[kPFull]);
           }
-          if (upd) {
-            wait(&bars[kKt], un++ & 1);
-            tc_fence_after();
-            auto term = [&](uint32_t col, uint32_t acc) {
-              mma4_tmem_a_run_warp<128>(tmem + kColU, tmem + col, vd, id_mn, acc);
-              mma4_tmem_a_run_warp<128>(tmem + kColU, tmem + col + 64, vd4, id_mn, 1);
-            };
-            term(kColE1, 0);
-            if (four) {
-              term(kColH2, 1);
-              term(kColT4, 1);
+          if (a || last || b + 1 < nb) {   // (the state after another segment comes from pass A)
+            const uint32_t q = a ? b & 1 : 0, used = q ? un1++ : un0++;
+            if (a && b >= 2) wait(&bars[kURead + q], (used - 1) & 1);
+            // pass A: all terms at once, half of the tokens after half; pass B: two terms at a time
+            const bool four = !kF16 && (a || last);
+#pragma unroll 1
+            for (int part = 0; part < (four && !a ? 2 : 1); ++part, ++tn) {
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                wait(&bars[kKt + h], tn & 1);
+                if (!a) wait(&bars[kKt + 1], tn & 1);   // (one accumulator: every warp has read it)
+                tc_fence_after();
+#pragma unroll 1
+                for (int t = four && a ? 3 : 1; t >= 0; --t)
+                  mma4_tmem_a_run_warp<128>(tmem + (q ? kColP : kColU), tmem + (t < 2 ? kColK : kColO) + 32 * (t & 1) + 64 * h,
+                                            desc_advance(vd, 8192 * h), id_mn,
+                                            h | part | (t != (four && a ? 3 : 1)));
+                if (a) mma_commit_warp(&bars[kHalf + h]);
+              }
+              if (four && !a && part == 0) {
+                mma_commit_warp(&bars[kHalf]);
+                mma_commit_warp(&bars[kHalf + 1]);
+              }
             }
-            term(kColHi, 1);
-            mma_commit_warp(&bars[kUFull]);
+            mma_commit_warp(&bars[kUFull + q]);
           }
-          if (pass == 1) {
-            wait(&bars[kPt], qn & 1);
+          if (!a) {
+            wait(&bars[kSReady], qn & 1);
             tc_fence_after();
-            const uint64_t qd = desc_kmajor(sbase + kQ, 0, 16384), sd = desc_mnmajor(sbase + kS, 0, 128, 16384);
-            mma_run_warp<4, 2, 128>(tmem + kColOi, qd, sd, id_mn, 0);
-            mma_run_warp<4, 2, 128>(tmem + kColOi, desc_advance(qd, 16384), desc_advance(sd, 4 * 2048), id_mn, 1);
-            mma4_tmem_a_run_warp<128>(tmem + kColOa, tmem + kColP, vd, id_mn, 0);
-            mma4_tmem_a_run_warp<128>(tmem + kColOa, tmem + kColP + 64, vd4, id_mn, 1);
+            const uint64_t sd = desc_mnmajor(sbase + kS, 0, 128, 16384);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              mma_run_warp<4, 2, 128>(tmem + kColO, desc_advance(qd, 16384 * h), desc_advance(sd, 8192 * h), id_mn, h);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              mma4_tmem_a_run_warp<128>(tmem + kColO, tmem + kColP + 64 * h, desc_advance(vd, 8192 * h), id_mn, 1);
             mma_commit_warp(&bars[kOFull]);
             ++qn;
           }
           mma_commit_warp(&bars[kKvEmpty + s]);
+        }
+        if (a) {   // both accumulators are read before pass B reuses their columns
+          wait(&bars[kURead], (un0 - 1) & 1);
+          if (nb > 1) wait(&bars[kURead + 1], (un1 - 1) & 1);
         }
       }
     }
@@ -635,7 +798,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       uint32_t* all = reinterpret_cast<uint32_t*>(p.ws);
       uint32_t* flags = all + cta * kFlagWords;
       uint32_t pubs0 = 0, pubs1 = 0, ins0 = 0, ins1 = 0, pn = 0;   // uses of this CTA's slots, by parity
-      for (uint32_t i = 0; next_item(i, it); ++i) {
+  #pragma unroll 1
+    for (uint32_t i = 0; next_item(i, it); ++i) {
         const int par = i & 1;
         const bool last = it.j + 1 == it.J;
         if (!last) {
@@ -645,7 +809,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           wait(&bars[kPub], pn++ & 1);
           if (lane == 0) {
             fence_acq_rel_gpu();
-            st_release_gpu(flags + kOutReady + par, i + 1);
+            st_relaxed_gpu(flags + kOutReady + par, i + 1);
           }
         }
         if (it.j > 0) {
@@ -653,16 +817,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           if (lane == 0) wait.flag(flags + kInCnt + par, kSlices * use);
           arrive_warp(&bars[kInReady]);
         }
-        wait(&bars[kGot], i & 1);
+        wait(&bars[kGot + (i & 3)], (i >> 2) & 1);
         if (lane == 0) {
           fence_acq_rel_gpu();
-          st_release_gpu(flags + kDone, i + 1);
+          st_relaxed_gpu(flags + kDone, i + 1);
         }
         if (last && it.J > 1) {
           // state_out may be state_in, whose reader is then the first segment
           if (lane == 0) wait.flag(all + (it.first % G) * kFlagWords + kDone, it.first / G + 1);
           arrive_warp(&bars[kOutOk]);
         }
+        arrive_warp(&bars[kItEmpty + (i & 3)]);
       }
     }
   } else if (warp >= kScanWarp) {
@@ -672,22 +837,27 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   } else {
     take_registers();
     // ----------------------------------------------------- compute warps ---
-    // Warp w4 of each half wg has lanes 32 w4 .. of tensor memory: rows (tokens) of P and
-    // o, columns (d_k) of K~ and of the state. wg: the half of the tokens of K~, of the
+    // Warp w4 of each four has lanes 32 w4 .. of tensor memory: rows (tokens) of P and o,
+    // columns (d_k) of K~ and of the state. wg: the half of the tokens of K~, of the
     // columns of P, and of d_v in o and the state.
     const int wg = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w4) << 16);
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w4) << 16) + 64 * wg;   // this warp's 64 columns of a region
     float* meta = reinterpret_cast<float*>(p.ws + Workspace::meta_offset(G)) + 2 * cta;
     uint8_t* slots = p.ws + Workspace::slots_offset(G) + (size_t)cta * 4 * kStateBytes;
-    const float log2_scale = log2f(p.scale);
-    uint32_t cnt = 0, tn = 0, qn = 0, un = 0, stn = 0, pn = 0, inn = 0, okn = 0, bn = 0, rn = 0;
+    uint32_t cnt = 0, qn = 0, rn = 0, phases = 0;   // phases: the parity that each barrier is waited for next
     float S[64];        // S[64 wg + i][row]
-    float s_up = 1.f;   // f16: the copy of S is S / s_up
+    float up = 1.f;     // f16: P' and the copy of S are divided by it
+    float seg_gam = 1.f;
 
+    auto wait_next = [&](int bar) {
+      wait(&bars[bar], (phases >> (bar - kUFull)) & 1);
+      phases ^= 1u << (bar - kUFull);
+    };
+    static_assert(kUFull < kHalf && kNumBars - kUFull <= 32, "one word of phases");
     // the compute warps' barrier
     auto sync = [&] {
       arrive_warp(&bars[kCBar]);
-      wait(&bars[kCBar], bn++ & 1);
+      wait_next(kCBar);
     };
     // the largest value over the compute threads (f16)
     auto reduce_max = [&](float m) {
@@ -698,20 +868,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       sync();
       m = red[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+      for (int i = 1; i < kComputeWarps; ++i) m = fmaxf(m, red[i]);
       return m;
     };
     // the rounded copy of S
-    auto write_copy = [&] {
-      float down = 1.f;
-      if constexpr (kF16) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(S[i]));
-        const int e = exponent_of(reduce_max(m)) - 14;   // the largest below 2^15
-        s_up = pow2i(e);
-        down = pow2i(-e);
-      }
+    auto write_copy = [&](float down) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         float x[8];
@@ -720,43 +881,39 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         *reinterpret_cast<uint4*>(sm + kS + wg * 16384 + row * 128 + ((c ^ (row & 7)) << 4)) = pack8<T>(x);
       }
       fence_async_smem();
+      arrive_warp(&bars[kSReady]);
     };
-    // The terms of K~ for tokens 64 wg .. + 63 and columns 32 w4 .. + 31 of K's tile at kt.
-    // Returns the power of two that they were multiplied with (f16).
+    // Sixteen registers of K's tile at kt: tokens 64 wg .. + 63, columns 32 w4 + 16 half .. + 15,
+    // as transposed pairs of tokens
     const uint32_t ldm_row = 64 * wg + 8 * ((lane >> 4) & 1) + (lane & 7);
-    auto make_terms = [&](uint32_t kt, int L, bool four) -> int {
-      uint32_t kr[32];
+    auto load_k = [&](uint32_t kt, int half, uint32_t* kr) {
+      const uint32_t c = 4 * w4 + 2 * half + ((lane >> 3) & 1);     // 16-byte chunk of K's row
+      const uint32_t at = sbase + kt + (c >> 3) * 16384 + ldm_row * 128 + (((c & 7) ^ (ldm_row & 7)) << 4);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t c = 4 * w4 + 2 * half + ((lane >> 3) & 1);     // 16-byte chunk of K's row
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const uint32_t r = ldm_row + 8 * i;
-          ldmatrix_t4(sbase + kt + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), kr + 16 * half + 2 * i);
-        }
-      }
-      if (L < kB) {   // rows behind the sequence may hold anything
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = 64 * wg + 8 * i + 2 * (lane & 3);
-          const uint32_t keep = (t < L ? 0xffffu : 0u) | (t + 1 < L ? 0xffff0000u : 0u);
-          kr[2 * i] &= keep; kr[2 * i + 1] &= keep; kr[16 + 2 * i] &= keep; kr[17 + 2 * i] &= keep;
-        }
-      }
+      for (int i = 0; i < 8; i += 2) ldmatrix_t4(at + 1024 * i, kr + 2 * i);
+    };
+    // Two terms of K~ (part 0: hi and, with four of them, e1; part 1: h2 and t4) or, for pass
+    // A, all four. Returns the power of two that they were multiplied with (f16).
+    auto put_terms = [&](uint32_t kt, bool four, bool all, int part) -> int {
       uint32_t w1[8], w2[8], w3[8];
       int e = 0;
       if constexpr (kF16) {
         __half2 m = __half2half2(__ushort_as_half(0));
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<__half2*>(&kr[i])));
+        for (int half = 0; half < 2; ++half) {
+          uint32_t kr[16];
+          load_k(kt, half, kr);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&kr[i])));
+        }
         const float2 f = __half22float2(m);
         // |w k| below 2^14 and w below 2^15
         e = min(13 - exponent_of(reduce_max(fmaxf(f.x, f.y)) * misc->w_max), 14 - exponent_of(misc->w_max));
-        const float up = pow2i(e);
+        const float scale = pow2i(e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float2 w = *reinterpret_cast<const float2*>(tab_w + 64 * wg + 8 * i + 2 * (lane & 3));
-          w.x *= up; w.y *= up;
+          w.x *= scale; w.y *= scale;
           w1[i] = Op16<T>::pack2(w.x, w.y);
           const float2 x = Op16<T>::unpack2(w1[i]);
           w2[i] = Op16<T>::pack2(w.x - x.x, w.y - x.y);
@@ -770,141 +927,182 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           w3[i] = tab_wp[128 + at];
         }
       }
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        const uint32_t tw = tl + (static_cast<uint32_t>(16 * half) << 16) + 64 * wg;
-        uint32_t x[16], y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] = Two<T>::mul(w1[i >> 1], kr[16 * half + i]);
-          y[i] = Two<T>::fma(w1[i >> 1], kr[16 * half + i], neg2(x[i]));
-        }
-        tmem_st_frag(tw + kColHi, x);
-        if (four) {
-          tmem_st_frag(tw + kColE1, y);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = Two<T>::mul(w2[i >> 1], kr[16 * half + i]);
-          tmem_st_frag(tw + kColH2, x);
+        uint32_t kr[16], x[16], y[16];
+        load_k(kt, half, kr);
+        const uint32_t tw = tl + kColK + (static_cast<uint32_t>(16 * half) << 16);
+        if (part == 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            y[i] = Two<T>::fma(w2[i >> 1], kr[16 * half + i], neg2(x[i]));
-            if constexpr (!kF16) y[i] = Two<T>::fma(w3[i >> 1], kr[16 * half + i], y[i]);
+            x[i] = Two<T>::mul(w1[i >> 1], kr[i]);
+            y[i] = Two<T>::fma(w1[i >> 1], kr[i], neg2(x[i]));
           }
-          tmem_st_frag(tw + kColT4, y);
-        } else {
+          if (!four) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = Two<T>::fma(w2[i >> 1], kr[16 * half + i], y[i]);
-          tmem_st_frag(tw + kColE1, y);
+            for (int i = 0; i < 16; ++i) y[i] = Two<T>::fma(w2[i >> 1], kr[i], y[i]);
+          }
+          tmem_st_frag(tw, x);
+          tmem_st_frag(tw + 32, y);
+        }
+        if (!kF16 && (all || part == 1)) {
+          const uint32_t tz = tw + (all ? kColO - kColK : 0u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            x[i] = Two<T>::mul(w2[i >> 1], kr[i]);
+            y[i] = Two<T>::fma(w2[i >> 1], kr[i], neg2(x[i]));
+            if constexpr (!kF16) y[i] = Two<T>::fma(w3[i >> 1], kr[i], y[i]);
+          }
+          tmem_st_frag(tz, x);
+          tmem_st_frag(tz + 32, y);
         }
       }
       tmem_wait_st();
       tc_fence_before();
-      arrive_warp(&bars[kKt]);
+      arrive_warp(&bars[kKt + wg]);
       return e;
     };
-    // rows of V behind the sequence: zero (their weights are, but they may hold anything)
-    auto clear_v = [&](uint32_t vt, int L) {
+    // Rows behind the sequence may hold anything: zero in V, and in the patch of K that this
+    // warp weighs (Q K^T masks its own).
+    auto clear_rows = [&](uint32_t kt, uint32_t vt, int L) {
+#pragma unroll 1
       for (int i = tid; i < (kB - L) * 16; i += kCompute) {
         const int r = L + (i >> 4), c = i & 15;
         *reinterpret_cast<uint4*>(sm + vt + (c >> 3) * 16384 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
       }
+#pragma unroll 1
+      for (int i = lane; i < 256; i += 32) {
+        const int r = 64 * wg + (i >> 2), c = 4 * w4 + (i & 3);
+        if (r >= L)
+          *reinterpret_cast<uint4*>(sm + kt + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+              make_uint4(0, 0, 0, 0);
+      }
       fence_async_smem();
+      __syncwarp();
     };
     // S <- exp(G_L) S + U
-    auto update_state = [&](float gam, float down) {
-      wait(&bars[kUFull], un++ & 1);
+    auto update_state = [&](int q, float gam, float down) {
+      wait_next(kUFull + q);
       tc_fence_after();
+      float u[64];
+      tmem_ld64(tl + (q ? kColP : kColU), u);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float u[32];
-        tmem_ld32(tl + kColU + 64 * wg + 32 * c, u);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) S[32 * c + i] = fmaf(gam, S[32 * c + i], kF16 ? u[i] * down : u[i]);
-      }
+      for (int i = 0; i < 64; ++i) S[i] = fmaf(gam, S[i], kF16 ? u[i] * down : u[i]);
       tc_fence_before();
+      arrive_warp(&bars[kURead + q]);
     };
-    // P, packed, over Q K^T. Returns the power of two that it was divided by (f16).
-    auto make_scores = [&](int L) -> float {
-      const float gr = tab_gp[row] + log2_scale;
-      uint32_t u[32];
-      auto scores = [&](float down) {
-        float top = 0.f, far = 0.f;
+    // f16: the power of two that P' and the copy of S share, from the larger of the two (so S
+    // has to be there): sets `up`, returns its inverse.
+    auto common_scale = [&](float top) {
 #pragma unroll
-        for (int c = 1; c >= 0; --c) {
-          const int cb = 2 * wg + c;               // columns 32 cb ..: zero above the diagonal
+      for (int i = 0; i < 64; ++i) top = fmaxf(top, fabsf(S[i]));
+      const int e = exponent_of(reduce_max(top)) - 14;   // the largest below 2^15
+      up = pow2i(e);
+      return pow2i(-e);
+    };
+    // P', packed, over Q K^T: 32 rows and 64 columns, zero above the diagonal.
+    auto make_scores = [&](int L) {
+      float down = 1.f, top = 0.f;
+#pragma unroll 1
+      for (int pass = kF16 ? 0 : 1; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int cb = 2 * wg + c;
+          uint32_t u[16];
           if (cb > w4) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[16 * c + i] = 0u;
-            continue;
-          }
-          float x[32];
-          tmem_ld32(tl + kColP + 32 * cb, x);
-          if (cb == w4) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 h4 = *reinterpret_cast<const float4*>(tab_gp + 32 * cb + i);
-              const float d[4] = {gr - h4.x, gr - h4.y, gr - h4.z, gr - h4.w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) x[i + y] = i + y <= lane ? x[i + y] * ex2(d[y]) : 0.f;
-            }
+            for (int i = 0; i < 16; ++i) u[i] = 0u;
           } else {
-            far = 0.f;
-            for (int y = cb + 1; y < w4; ++y) far += misc->tot[y];
-            const float a = ex2(gr + far);
+            float x[32];
+            tmem_ld32(tl + kColP + 32 * c, x);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 b4 = *reinterpret_cast<const float4*>(tab_gb + 32 * cb + i);
-              x[i] *= b4.x * a; x[i + 1] *= b4.y * a; x[i + 2] *= b4.z * a; x[i + 3] *= b4.w * a;
+            for (int i = 0; i < 8; ++i) {
+              const float4 b = *reinterpret_cast<const float4*>(tab_gb + 32 * cb + 4 * i);
+              x[4 * i] *= b.x; x[4 * i + 1] *= b.y; x[4 * i + 2] *= b.z; x[4 * i + 3] *= b.w;
             }
-          }
-          if constexpr (kF16) {
+            if (cb == w4) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              top = fmaxf(top, fabsf(x[i]));
-              x[i] *= down;
+              for (int i = 0; i < 32; ++i) x[i] = i <= lane ? x[i] : 0.f;
             }
-          }
+            if constexpr (kF16) {
+              if (pass == 0) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) u[16 * c + i] = Op16<T>::pack2(x[2 * i], x[2 * i + 1]);
+                for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] *= down;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = Op16<T>::pack2(x[2 * i], x[2 * i + 1]);
+          }
+          if (pass == 1) tmem_st16(tl + kColP + 16 * c, u);   // (columns that this warp has read)
         }
-        return row < L ? top : 0.f;
-      };
-      const float top = scores(1.f);
-      float up = 1.f;
-      if constexpr (kF16) {
-        const float most = reduce_max(top);
-        if (most >= 32768.f) {
-          const int e = exponent_of(most) - 14;
-          up = pow2i(e);
-          scores(pow2i(-e));
+        if constexpr (kF16) {
+          if (pass == 0) down = common_scale(row < L ? top : 0.f);
         }
       }
-      tmem_st16(tl + kColP + 64 * wg, u);
-      tmem_st16(tl + kColP + 64 * wg + 16, u + 16);
       tmem_wait_st();
       tc_fence_before();
-      arrive_warp(&bars[kPt]);
-      return up;
+      return down;
     };
-    // o of this warp's 32 tokens and 64 columns, through its own part of kO
-    uint8_t* o_stage = sm + kO + wg * 16384 + w4 * 4096;
+    // A steep block's: 2^-m_r out of a row of Q, and P' by the exponent; compact, not fast.
+    auto make_steep_scores = [&](int L, uint8_t* q, int m_row) {
+      const float f = m_row > 126 ? 0.f : pow2i(-m_row);
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(q + wg * 16384 + row * 128 + ((c ^ (row & 7)) << 4));
+        float x[8];
+        unpack8<T>(*at, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= f;
+        *at = pack8<T>(x);
+      }
+      float down = 1.f, top = 0.f;
+#pragma unroll 1
+      for (int pass = kF16 ? 0 : 1; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          const int col = 64 * wg + 8 * c, cb = col >> 5;
+          const float far = (float)(-misc->start_i[cb] - m_row) - misc->start_f[cb];
+          float x[8];
+          tmem_ld8(tl + kColP + 8 * c, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = col + i <= row ? x[i] * ex2(far + tab_gp[col + i]) : 0.f;
+            top = fmaxf(top, fabsf(x[i]));
+          }
+          if (pass == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tmem_st1(tl + kColP + 4 * c + i, Op16<T>::pack2(x[2 * i] * down, x[2 * i + 1] * down));
+          }
+        }
+        if constexpr (kF16) {
+          if (pass == 0) down = common_scale(row < L ? top : 0.f);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      return down;
+    };
+    // o of this warp's 32 tokens and 64 columns, through its part of the block's Q buffer
     const int o_chunks = min(8, max(0, p.dv / 8 - 8 * wg));    // 16-byte chunks of these columns
-    auto write_o = [&](int t, int h, int L, float row_gam, float up) {
+    auto stage_o = [&](uint8_t* o_stage, float rho) {
       if (o_chunks == 0) return;
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
+#pragma unroll 1
+      for (int c = 0; c < 8; c += 4) {
+        float x[32];
+        tmem_ld32(tl + kColO + 8 * c, x);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[16], y[16];
-        tmem_ld16(tl + kColOi + 64 * wg + 16 * c, x);
-        tmem_ld16(tl + kColOa + 64 * wg + 16 * c, y);
+        for (int i = 0; i < 32; ++i) x[i] *= rho;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = fmaf(row_gam, x[i], kF16 ? y[i] * up : y[i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4*>(o_stage + lane * 128 + (((2 * c + i) ^ (lane & 7)) << 4)) = pack8<T>(x + 8 * i);
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(o_stage + lane * 128 + (((c + i) ^ (lane & 7)) << 4)) = pack8<T>(x + 8 * i);
       }
       tc_fence_before();
+    };
+    auto send_o = [&](const uint8_t* o_stage, int t, int h, int L) {
+      if (o_chunks == 0) return;
       const int rows = min(32, L - 32 * w4);
       if (rows == 32) {
         fence_async_smem();
@@ -915,120 +1113,158 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         }
       } else {
         __syncwarp();
-        T* o = static_cast<T*>(p.o);
-        for (int i = lane; i < rows * o_chunks; i += 32) {
-          const int r = i / o_chunks, c = i - r * o_chunks;
-          __stcs(reinterpret_cast<uint4*>(o + ((size_t)(t + 32 * w4 + r) * p.Hv + h) * p.dv + 64 * wg + 8 * c),
-                 *reinterpret_cast<const uint4*>(o_stage + r * 128 + ((c ^ (r & 7)) << 4)));
+        T* o = static_cast<T*>(p.o) + ((size_t)(t + 32 * w4) * p.Hv + h) * p.dv + 64 * wg;
+        const int c = lane & 7;
+        if (c < o_chunks) {
+#pragma unroll 1
+          for (int r = lane >> 3; r < rows; r += 4)
+            __stcs(reinterpret_cast<uint4*>(o + (size_t)r * p.Hv * p.dv + 8 * c),
+                   *reinterpret_cast<const uint4*>(o_stage + r * 128 + ((c ^ (r & 7)) << 4)));
         }
       }
     };
-    // element (d_v 64 wg + i, d_k row) of a staged state: boxes of 32 columns, 128-byte rows
-    auto staged = [&](int i) {
-      const int v = 64 * wg + i;
-      return reinterpret_cast<float*>(sm + kStage + w4 * 16384 + v * 128 + (((lane >> 2) ^ (v & 7)) << 4) + (lane & 3) * 4);
-    };
-
+#pragma unroll 1
     for (uint32_t i = 0; next_item(i, it); ++i) {
       const int nb = (it.len + kB - 1) / kB, par = i & 1;
       const bool last = it.j + 1 == it.J;
-      if (!last) {
-        // --------------------------------------------------------- pass A ---
+      // One body for both passes. K~ of a block is made while the tensor core is at the block
+      // before it: in pass A the state follows a block behind; in pass B o of the block before
+      // leaves tensor memory first, because K~ goes where it was.
+#pragma unroll 1
+      for (int pass = last ? 1 : 0; pass < 2; ++pass) {
+        if (pass == 0) {
 #pragma unroll
-        for (int x = 0; x < 64; ++x) S[x] = 0.f;
-        float seg_gam = 1.f;
-        for (int b = 0; b < nb && wait.ok; ++b, ++cnt) {
-          const uint32_t s = cnt & 1;
-          wait(&bars[kTabFull], tn++ & 1);
-          wait(&bars[kKvFull + s], (cnt >> 1) & 1);
-          const float gam = misc->gam_l;
-          seg_gam = misc->seg_gam;
-          const int e = make_terms(kK + s * 32768, kB, !kF16);   // (only a last segment has a short block)
-          arrive_warp(&bars[kTabEmpty]);
-          update_state(gam, pow2i(-e));
+          for (int x = 0; x < 64; ++x) S[x] = 0.f;
         }
-        wait(&bars[kSlotFree], pn++ & 1);
-        float4* out = reinterpret_cast<float4*>(slots + (size_t)par * kStateBytes);
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          __stcg(out + 256 * v + tid, make_float4(S[4 * v], S[4 * v + 1], S[4 * v + 2], S[4 * v + 3]));
-        if (tid == 0) __stcg(meta + par, seg_gam);
-        arrive_warp(&bars[kPub]);
-      }
-      // ----------------------------------------------------------- pass B ---
-      // the state that enters
-      if (it.j > 0) {
-        wait(&bars[kInReady], inn++ & 1);
-        const float4* in = reinterpret_cast<const float4*>(slots + (size_t)(2 + par) * kStateBytes);
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const float4 x = __ldcg(in + 256 * v + tid);
-          S[4 * v] = x.x; S[4 * v + 1] = x.y; S[4 * v + 2] = x.z; S[4 * v + 3] = x.w;
-        }
-      } else if (p.state_in) {
-        const int boxes = (p.dk + 31) / 32;
-        if (lane == 0) bulk_wait_read_all();   // (what went out through kS and kO)
-        fence_async_smem();
-        sync();
-        if (tid == 0) {
-          mbar_arrive_expect_tx(&bars[kStFull], boxes * 16384);
-          for (int x = 0; x < boxes; ++x)
-            tma_load_3d(sm + kStage + x * 16384, &sim, &bars[kStFull], 32 * x, 0, it.n * p.Hv + it.h);
-        }
-        wait(&bars[kStFull], stn++ & 1);
-#pragma unroll
-        for (int x = 0; x < 64; ++x) S[x] = w4 < boxes ? *staged(x) : 0.f;
-        sync();
-      } else {
-#pragma unroll
-        for (int x = 0; x < 64; ++x) S[x] = 0.f;
-      }
-      if (nb > 0) {
-        // kS may be a state's on its way out (thread 0's stores)
-        if (i > 0 && !(it.j == 0 && p.state_in)) {
-          if (tid == 0) bulk_wait_read_all();
-          sync();
-        }
-        write_copy();
-      }
-      if (p.ws) arrive_warp(&bars[kGot]);
-      for (int b = 0; b < nb && wait.ok; ++b, ++cnt, ++qn) {
-        const uint32_t s = cnt & 1;
-        const int t = it.t0 + b * kB, L = min(kB, it.len - b * kB);
-        const bool upd = last || b + 1 < nb;
-        wait(&bars[kTabFull], tn++ & 1);
-        wait(&bars[kKvFull + s], (cnt >> 1) & 1);
-        const float gam = misc->gam_l, row_gam = tab_gam[row] * s_up;
-        if (L < kB) clear_v(kV + s * 32768, L);
+        float gam = 0.f, rho = 0.f;
         int e = 0;
-        if (upd) e = make_terms(kK + s * 32768, L, !kF16 && last);
-        wait(&bars[kPFull], qn & 1);
-        tc_fence_after();
-        const float up = make_scores(L);
-        arrive_warp(&bars[kTabEmpty]);
-        if (upd) update_state(gam, pow2i(-e));
-        wait(&bars[kOFull], qn & 1);
-        tc_fence_after();
-        write_o(t, it.h, L, row_gam, up);
-        if (upd && b + 1 < nb) write_copy();
+#pragma unroll 1
+        for (int b = 0; b <= nb && wait.ok(); ++b) {
+          const bool a = each_time(pass == 0), ends = each_time(last);
+          const uint32_t s = cnt & 1;
+          const int L = min(kB, it.len - b * kB);
+          const bool here = each_time(b < nb), upd = each_time(here && (a || ends || b + 1 < nb));
+          const bool four = !kF16 && (a || ends);
+          const float gam_before = gam, rho_before = rho;
+          const int e_before = e;
+          float down = 1.f;
+          uint8_t* const q_tile = sm + kQ + (qn & 1) * 32768;
+          if (here) {
+            wait(&bars[kKvFull + s], (cnt >> 1) & 1);
+            gam = misc->gam_l;
+            if (L < kB) clear_rows(kK + s * 32768, kV + s * 32768, L);
+          }
+          // four terms of K~ outside pass A: the second two when the first are multiplied
+          const int parts = each_time(four && !a && upd) ? 2 : 1;
+#pragma unroll 1
+          for (int part = 0; part < parts; ++part) {
+            if (part == 1 || (a && b > 0)) wait_next(kHalf + wg);
+            if (upd) e = put_terms(kK + s * 32768, four, a, part);
+            if (part == 1) {
+              arrive_warp(&bars[kTabEmpty]);
+              break;
+            }
+            if (!a && b == 0) {
+              // the state that enters
+              if (it.j > 0) {
+                wait_next(kInReady);
+                const float4* in = reinterpret_cast<const float4*>(slots + (size_t)(2 + par) * kStateBytes);
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                  const float4 x = __ldcg(in + 256 * v + tid);
+                  S[4 * v] = x.x; S[4 * v + 1] = x.y; S[4 * v + 2] = x.z; S[4 * v + 3] = x.w;
+                }
+              } else {
+                const float* in = p.state_in + (((size_t)it.n * p.Hv + it.h) * p.dv + 64 * wg) * p.dk + row;
+                if (!p.state_in) {
+#pragma unroll
+                  for (int x = 0; x < 64; ++x) S[x] = 0.f;
+                } else if (kWhole) {
+#pragma unroll
+                  for (int x = 0; x < 64; ++x) S[x] = __ldcs(in + x * kD);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 64; ++x) S[x] = row < p.dk && 64 * wg + x < p.dv ? __ldcs(in + x * p.dk) : 0.f;
+                }
+              }
+            }
+            if (!a && here) {
+              const bool steep = each_time(misc->steep != 0);
+              wait_next(kPFull);
+              tc_fence_after();
+              rho = tab_gam[row];
+              if (steep) {
+                const float rest = misc->start_f[w4] - tab_gp[row];
+                const int m_row = max(0, -kSteep<T> - misc->start_i[w4] - (int)ceilf(rest));
+                rho = p.scale * ex2((float)(misc->start_i[w4] + m_row) + rest);
+                down = make_steep_scores(L, q_tile, m_row);
+              } else {
+                down = make_scores(L);
+              }
+            }
+            if (here) {
+              if (a && b + 1 == nb) seg_gam = misc->seg_gam;
+              if (a || !four || !upd) arrive_warp(&bars[kTabEmpty]);
+            }
+            if (!a) {
+              if (here) rho *= up;
+              if (b > 0) {
+                uint8_t* const o_stage = sm + kQ + (~qn & 1) * 32768 + wg * 16384 + w4 * 4096;
+                wait_next(kOFull);
+                tc_fence_after();
+                stage_o(o_stage, rho_before);
+                send_o(o_stage, it.t0 + (b - 1) * kB, it.h, min(kB, it.len - (b - 1) * kB));
+              }
+              if (here) write_copy(down);
+              if (p.ws && b == 0) arrive_warp(&bars[kGot + (i & 3)]);
+            }
+          }
+          if (!a) {
+            if (b > 0) {   // the Q buffer is free when o has left it
+              if (lane == 0) bulk_wait_read_all();
+              arrive_warp(&bars[kQFree + (~qn & 1)]);
+            }
+            if (here) ++qn;
+          }
+          if (here) ++cnt;
+          if (a ? b > 0 : upd) update_state(a ? ~b & 1 : 0, a ? gam_before : gam, pow2i(a ? -e_before : -e));
+        }
+        if (pass == 0) {
+          wait_next(kSlotFree);
+          float4* out = reinterpret_cast<float4*>(slots + (size_t)par * kStateBytes);
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            __stcg(out + 256 * v + tid, make_float4(S[4 * v], S[4 * v + 1], S[4 * v + 2], S[4 * v + 3]));
+          if (tid == 0) __stcg(meta + par, seg_gam);
+          arrive_warp(&bars[kPub]);
+        }
       }
       if (last) {
-        // the state after the sequence
-        if (it.J > 1) wait(&bars[kOutOk], okn++ & 1);
-        if (lane == 0) bulk_wait_read_all();
-        sync();
+        // the state after the sequence: a row of 32 consecutive columns a store
+        if (it.J > 1) wait_next(kOutOk);
+        float* out = p.state_out + (((size_t)it.n * p.Hv + it.h) * p.dv + 64 * wg) * p.dk + row;
+        if (kWhole) {
 #pragma unroll
-        for (int x = 0; x < 64; ++x) *staged(x) = S[x];
-        fence_async_smem();
-        sync();
-        if (tid == 0) {
-          for (int x = 0; 32 * x < p.dk; ++x)
-            tma_store_3d(&som, sm + kStage + x * 16384, 32 * x, 0, it.n * p.Hv + it.h);
-          bulk_commit_group();
+          for (int x = 0; x < 64; ++x) __stcs(out + x * kD, S[x]);
+        } else if (row < p.dk) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (64 * wg + x < p.dv) __stcs(out + x * p.dk, S[x]);
         }
       }
     }
     if (lane == 0) bulk_wait_all();
+  }
+  if (warp < kWarps - 1) {
+    arrive_warp(&bars[kLeft]);
+  } else {   // the watchdog
+    const long long t0 = clock64();
+    while (!mbar_try_wait(&bars[kLeft], 0)) {
+      if (clock64() - t0 > p.limit) {
+        wait.give_up();
+        break;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1036,6 +1272,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (tid == 0 && !wait.ok()) flag_error(kErrTimeout);
 }
 
 }  // namespace ltc
