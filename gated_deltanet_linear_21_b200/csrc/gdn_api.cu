@@ -381,7 +381,7 @@ bool linear_on_tensor_cores(gdn_dtype dtype, int64_t total_T) { return dtype != 
 int linear_segment(int n_seqs, int64_t total_T, int Hv) {
   const int64_t per_seq = std::max<int64_t>(1, (total_T / std::max(1, n_seqs) + 127) / 128);
   const int64_t blocks = per_seq * n_seqs * Hv;
-  return (int)std::min<int64_t>(4, std::max<int64_t>(1, (blocks + kLinearCtas - 1) / kLinearCtas));
+  return (int)std::min<int64_t>(8, std::max<int64_t>(1, (blocks + kLinearCtas - 1) / kLinearCtas));
 }
 
 template <typename T>

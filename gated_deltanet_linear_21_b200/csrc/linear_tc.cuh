@@ -539,10 +539,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const bool warps = (i >= kGot && i < kGot + 4) || i == kURead || i == kURead + 1 || i == kQFree || i == kQFree + 1 ||
-                         i == kTabEmpty || i == kSReady || i == kPub || i == kCBar;
+                         i == kTabEmpty || i == kSReady || i == kKt || i == kKt + 1 || i == kPub || i == kCBar;
       const bool readers = i >= kItEmpty && i < kItEmpty + kRingItems, both = i == kKvFull || i == kKvFull + 1;
-      mbar_init(&bars[i], warps ? kComputeWarps : i == kKt || i == kKt + 1 ? kComputeWarps / 2
-                          : readers ? kComputeWarps + (p.ws ? 3 : 2) : i == kLeft ? kWarps - 1 : both ? 2 : 1);
+      mbar_init(&bars[i], warps ? kComputeWarps : readers ? kComputeWarps + (p.ws ? 3 : 2) : i == kLeft ? kWarps - 1 : both ? 2 : 1);
     }
     fence_mbar_init();
     misc->dead = 0;
@@ -720,7 +719,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     constexpr uint32_t id_qk = idesc_f16kind(128, 128, false, false, kFmt);   // both K-major
     constexpr uint32_t id_mn = idesc_f16kind(128, 128, false, true, kFmt);    // B MN-major
     // (one copy of each product's code: the loops of all roles share the instruction cache)
-    uint32_t cnt = 0, qn = 0, tn = 0, un0 = 0, un1 = 0;   // tn: K~s; un: uses of either accumulator
+    uint32_t cnt = 0, qn = 0, tn0 = 0, tn1 = 0, un0 = 0, un1 = 0;   // tn, un: uses of kKt and the accumulators
 #pragma unroll 1
     for (uint32_t i = 0; next_item(i, it); ++i) {
       const int nb = (it.len + kB - 1) / kB;
@@ -747,26 +746,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           if (a || last || b + 1 < nb) {   // (the state after another segment comes from pass A)
             const uint32_t q = a ? b & 1 : 0, used = q ? un1++ : un0++;
             if (a && b >= 2) wait(&bars[kURead + q], (used - 1) & 1);
-            // pass A: all terms at once, half of the tokens after half; pass B: two terms at a time
-            const bool four = !kF16 && (a || last);
+            // Two terms of K~ at a time. Pass A has room for two such pairs, so one is made while
+            // the other is multiplied: the block's other two (bf16), or the next block's (f16).
+            const int parts = !kF16 && (a || last) ? 2 : 1;
 #pragma unroll 1
-            for (int part = 0; part < (four && !a ? 2 : 1); ++part, ++tn) {
+            for (int part = 0; part < parts; ++part) {
+              const uint32_t r = parts == 2 ? part : a ? b & 1 : 0;
+              wait(&bars[kKt + r], (r ? tn1++ : tn0++) & 1);
+              tc_fence_after();
 #pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                wait(&bars[kKt + h], tn & 1);
-                if (!a) wait(&bars[kKt + 1], tn & 1);   // (one accumulator: every warp has read it)
-                tc_fence_after();
-#pragma unroll 1
-                for (int t = four && a ? 3 : 1; t >= 0; --t)
-                  mma4_tmem_a_run_warp<128>(tmem + (q ? kColP : kColU), tmem + (t < 2 ? kColK : kColO) + 32 * (t & 1) + 64 * h,
-                                            desc_advance(vd, 8192 * h), id_mn,
-                                            h | part | (t != (four && a ? 3 : 1)));
-                if (a) mma_commit_warp(&bars[kHalf + h]);
-              }
-              if (four && !a && part == 0) {
-                mma_commit_warp(&bars[kHalf]);
-                mma_commit_warp(&bars[kHalf + 1]);
-              }
+              for (int x = 0; x < 4; ++x)   // the smaller term first, either half of the tokens
+                mma4_tmem_a_run_warp<128>(tmem + (q ? kColP : kColU),
+                                          tmem + (a && r ? kColO : kColK) + (x < 2 ? 32 : 0) + 64 * (x & 1),
+                                          desc_advance(vd, 8192 * (x & 1)), id_mn, part | x);
+              if (a || part + 1 < parts) mma_commit_warp(&bars[kHalf + r]);
             }
             mma_commit_warp(&bars[kUFull + q]);
           }
@@ -892,9 +885,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
 #pragma unroll
       for (int i = 0; i < 8; i += 2) ldmatrix_t4(at + 1024 * i, kr + 2 * i);
     };
-    // Two terms of K~ (part 0: hi and, with four of them, e1; part 1: h2 and t4) or, for pass
-    // A, all four. Returns the power of two that they were multiplied with (f16).
-    auto put_terms = [&](uint32_t kt, bool four, bool all, int part) -> int {
+    // Two terms of K~ (part 0: hi and, with four of them, e1; part 1: h2 and t4). Returns the
+    // power of two that they were multiplied with (f16).
+    auto put_terms = [&](uint32_t kt, bool four, int part, uint32_t region, int bar) -> int {
       uint32_t w1[8], w2[8], w3[8];
       int e = 0;
       if constexpr (kF16) {
@@ -931,7 +924,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       for (int half = 0; half < 2; ++half) {
         uint32_t kr[16], x[16], y[16];
         load_k(kt, half, kr);
-        const uint32_t tw = tl + kColK + (static_cast<uint32_t>(16 * half) << 16);
+        const uint32_t tw = tl + region + (static_cast<uint32_t>(16 * half) << 16);
         if (part == 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -942,24 +935,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[i] = Two<T>::fma(w2[i >> 1], kr[i], y[i]);
           }
-          tmem_st_frag(tw, x);
-          tmem_st_frag(tw + 32, y);
-        }
-        if (!kF16 && (all || part == 1)) {
-          const uint32_t tz = tw + (all ? kColO - kColK : 0u);
+        } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             x[i] = Two<T>::mul(w2[i >> 1], kr[i]);
             y[i] = Two<T>::fma(w2[i >> 1], kr[i], neg2(x[i]));
             if constexpr (!kF16) y[i] = Two<T>::fma(w3[i >> 1], kr[i], y[i]);
           }
-          tmem_st_frag(tz, x);
-          tmem_st_frag(tz + 32, y);
         }
+        tmem_st_frag(tw, x);
+        tmem_st_frag(tw + 32, y);
       }
       tmem_wait_st();
       tc_fence_before();
-      arrive_warp(&bars[kKt + wg]);
+      arrive_warp(&bars[kKt + bar]);
       return e;
     };
     // Rows behind the sequence may hold anything: zero in V, and in the patch of K that this
@@ -1154,16 +1143,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             gam = misc->gam_l;
             if (L < kB) clear_rows(kK + s * 32768, kV + s * 32768, L);
           }
-          // four terms of K~ outside pass A: the second two when the first are multiplied
-          const int parts = each_time(four && !a && upd) ? 2 : 1;
+          // K~: two terms, and with four of them two more -- in pass A beside the first, else when
+          // those are multiplied
+          const int parts = each_time(four && (a || upd)) ? 2 : 1;
 #pragma unroll 1
           for (int part = 0; part < parts; ++part) {
-            if (part == 1 || (a && b > 0)) wait_next(kHalf + wg);
-            if (upd) e = put_terms(kK + s * 32768, four, a, part);
-            if (part == 1) {
+            const int r = four ? part : a ? b & 1 : 0;
+            if (a ? b >= (four ? 1 : 2) : part == 1) wait_next(kHalf + (a ? r : 0));
+            if (a && !four && !here) wait_next(kHalf + (~b & 1));
+            if (upd) e = put_terms(kK + s * 32768, four, part, a && r ? kColO : kColK, r);
+            if (part + 1 == parts && here && (a || four)) {
+              if (a && b + 1 == nb) seg_gam = misc->seg_gam;
               arrive_warp(&bars[kTabEmpty]);
-              break;
             }
+            if (a || part == 1) continue;
             if (!a && b == 0) {
               // the state that enters
               if (it.j > 0) {
@@ -1202,10 +1195,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
                 down = make_scores(L);
               }
             }
-            if (here) {
-              if (a && b + 1 == nb) seg_gam = misc->seg_gam;
-              if (a || !four || !upd) arrive_warp(&bars[kTabEmpty]);
-            }
+            if (here && !four) arrive_warp(&bars[kTabEmpty]);
             if (!a) {
               if (here) rho *= up;
               if (b > 0) {
