@@ -384,6 +384,25 @@ int linear_segment(int n_seqs, int64_t total_T, int Hv) {
   return (int)std::min<int64_t>(8, std::max<int64_t>(1, (blocks + kLinearCtas - 1) / kLinearCtas));
 }
 
+// fp32: tokens per segment, so that about 2400 CTAs of one segment's 32 state rows each
+// are at work, and the workspace of the segments' states: what precedes the states holds
+// their decays.
+struct ScanPlan {
+  int seg;
+  int64_t segments;    // at most
+  size_t decay_bytes, bytes;
+};
+ScanPlan scan_plan(int n_seqs, int64_t total_T, int Hv, int dk, int dv) {
+  ScanPlan s;
+  const int64_t rows = (dv + gdn::lin::kScanRows - 1) / gdn::lin::kScanRows;
+  const int64_t blocks = (total_T * Hv * rows / 2400 + 63) / 64;
+  s.seg = (int)(64 * std::max<int64_t>(1, blocks));
+  s.segments = total_T / s.seg + n_seqs;
+  s.decay_bytes = ((size_t)s.segments * Hv * 4 + 255) & ~size_t(255);
+  s.bytes = total_T <= s.seg ? 0 : s.decay_bytes + (size_t)s.segments * Hv * dv * dk * 4;
+  return s;
+}
+
 template <typename T>
 gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const void* v, int64_t total_T,
                             gdn::ltc::Params prm, CUtensorMapDataType ty, cudaStream_t st) {
@@ -491,9 +510,8 @@ gdn_status with_pool_types(gdn_code code, gdn_dtype state_dtype, int dk, F f) {
 extern "C" {
 
 size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype) {
-  (void)dk;
-  (void)dv;
-  if (n_seqs <= 0 || Hv <= 0 || !linear_on_tensor_cores(dtype, total_T)) return 0;
+  if (n_seqs <= 0 || Hv <= 0 || total_T <= 0) return 0;
+  if (!linear_on_tensor_cores(dtype, total_T)) return scan_plan(n_seqs, total_T, Hv, dk, dv).bytes;
   // sequences of one segment need none
   if (total_T <= (int64_t)linear_segment(n_seqs, total_T, Hv) * gdn::ltc::kB) return 0;
   return gdn::ltc::Workspace::bytes(kLinearCtas);
@@ -556,16 +574,38 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
       return launch_linear_tc<__half>(fn, q, k, v, total_T, prm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, st);
     return launch_linear_tc<__nv_bfloat16>(fn, q, k, v, total_T, prm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, st);
   }
-  return with_dtype(dtype, [&](auto* tag) {
-    using T = std::remove_pointer_t<decltype(tag)>;
-    return with_dk(dk, [&](auto dkc) {
-      const dim3 grid((unsigned)((dv + gdn::lin::kScanRows - 1) / gdn::lin::kScanRows), (unsigned)Hv, (unsigned)n_seqs);
-      gdn::lin::scan_kernel<T, decltype(dkc)::value>
-          <<<grid, gdn::lin::kScanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-              static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_stride, state_in,
-              cu_seqlens, Hqk, Hv, dv, scale, static_cast<T*>(o), state_out, (long long)total_T);
-      return launch_status(fn);
-    });
+  // fp32 (and no tokens at all, where only the states are copied)
+  const ScanPlan plan = scan_plan(n_seqs, total_T, Hv, dk, dv);
+  gdn::lin::ScanParams prm = {};
+  prm.g = g;
+  prm.state_in = state_in;
+  prm.cu_seqlens = cu_seqlens;
+  prm.state_out = state_out;
+  prm.decays = static_cast<float*>(workspace);
+  prm.states = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.decay_bytes);
+  prm.g_stride = g_stride;
+  prm.n_seqs = n_seqs;
+  prm.total_T = (int)total_T;
+  prm.Hqk = Hqk;
+  prm.Hv = Hv;
+  prm.dv = dv;
+  prm.seg = plan.seg;
+  prm.scale = scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_dk(dk, [&](auto dkc) {
+    constexpr int DK = decltype(dkc)::value;
+    const dim3 grid((unsigned)plan.segments, (unsigned)Hv, (unsigned)((dv + gdn::lin::kScanRows - 1) / gdn::lin::kScanRows));
+    const auto *qf = static_cast<const float*>(q), *kf = static_cast<const float*>(k), *vf = static_cast<const float*>(v);
+    auto* of = static_cast<float*>(o);
+    if (need > 0) {
+      gdn::lin::scan_kernel<float, DK, false><<<grid, gdn::lin::kScanThreads, 0, st>>>(qf, kf, vf, of, prm);
+      if (gdn_status s = launch_status(fn)) return s;
+      gdn::lin::combine_kernel<<<dim3((unsigned)((dv * DK + 1023) / 1024), (unsigned)Hv, (unsigned)n_seqs), 256, 0, st>>>(
+          prm, dv * DK);
+      if (gdn_status s = launch_status(fn)) return s;
+    }
+    gdn::lin::scan_kernel<float, DK, true><<<grid, gdn::lin::kScanThreads, 0, st>>>(qf, kf, vf, of, prm);
+    return launch_status(fn);
   });
 }
 
