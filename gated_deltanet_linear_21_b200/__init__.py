@@ -285,14 +285,28 @@ def device_error(stream=None) -> None:
 
 
 # ------------------------------------------------------- linear attention ---
-def _on(device, **tensors):
-    """The tensors (None: left out) are all on `device`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, is on {t.device}")
-
-
+# The checks are written so that a good call costs a few comparisons: a step of one
+# token takes the GPU a few microseconds. Where one fails, _explain names the argument.
+_fns = {}
 _here = contextlib.nullcontext()
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    return f
+
+
+def _fits(t, dtype, shape, device):
+    return t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()
+
+
+def _explain(t, name, dtype, shape, device):
+    """Raises for an argument that _fits refuses."""
+    _dev(t, name, dtype)
+    _shape(t, name, shape)
+    raise ValueError(f"{name} must be on {device}, is on {t.device}")
 
 
 def _running_on(device, stream):
@@ -306,17 +320,40 @@ def _running_on(device, stream):
     return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _decay(g, rows, Hv):
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _qkv(q, k, v, rows):
+    """Checks q, k [rows, Hqk, dk], v [rows, Hv, dv] of one type; (device, dtype code, Hqk, dk, Hv, dv)."""
+    if not (isinstance(q, torch.Tensor) and isinstance(v, torch.Tensor) and q.is_cuda and q.is_contiguous()):
+        _dev(q, "q"); _dev(v, "v")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q, k must be [{rows}, Hqk, dk] and v [{rows}, Hv, dv]")
+    dtype, device = q.dtype, q.device
+    n, Hqk, dk = q.shape
+    _, Hv, dv = v.shape
+    if not (isinstance(k, torch.Tensor) and _fits(k, dtype, q.shape, device)):
+        _explain(k, "k", dtype, (n, Hqk, dk), device)
+    if not _fits(v, dtype, (n, Hv, dv), device):
+        _explain(v, "v", dtype, (n, Hv, dv), device)
+    return device, _dtype_code(q), n, Hqk, dk, Hv, dv
+
+
+def _decay(g, rows, Hv, device):
     """The token stride of log-decays [rows, Hv] or [Hv]."""
-    _dev(g, "g", torch.float32)
-    if tuple(g.shape) == (Hv,):
+    if not isinstance(g, torch.Tensor) or g.dtype != torch.float32 or g.device != device or not g.is_contiguous():
+        _dev(g, "g", torch.float32)
+        raise ValueError(f"g must be on {device}, is on {g.device}")
+    if g.shape == (Hv,):
         return 0
     _shape(g, "g", (rows, Hv))
     return Hv
 
 
 def linear_prefill_workspace_bytes(n_seqs, total_T, Hv, dk, dv, dtype=torch.bfloat16) -> int:
-    return int(lib().gdn_linear_prefill_workspace_bytes(n_seqs, total_T, Hv, dk, dv, _torch_dtype_code(dtype)))
+    """Bytes of workspace that linear_prefill takes for n_seqs packed sequences of total_T tokens."""
+    return _fn("gdn_linear_prefill_workspace_bytes")(n_seqs, total_T, Hv, dk, dv, _torch_dtype_code(dtype))
 
 
 def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=None, state_out=None,
@@ -328,44 +365,43 @@ def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=
     [T, Hv], or [Hv] for a decay fixed per value head; state_in [N, Hv, dv, dk]
     fp32 or None; cu_seqlens [N+1] int32 (None = one sequence of T tokens).
     state_out may be state_in. Returns (o [T, Hv, dv], state_out [N, Hv, dv, dk]).
+    What the call allocates belongs to the stream it runs on.
     """
-    _dev(q, "q"); _dev(k, "k", q.dtype); _dev(v, "v", q.dtype)
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k must be [T, Hqk, dk] and v [T, Hv, dv]")
-    dtype = _dtype_code(q)
-    T, Hqk, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[2]
-    _shape(k, "k", (T, Hqk, dk)); _shape(v, "v", (T, Hv, dv))
-    g_stride = _decay(g, T, Hv)
-    with _running_on(q.device, stream):
+    device, code, T, Hqk, dk, Hv, dv = _qkv(q, k, v, "T")
+    g_stride = _decay(g, T, Hv, device)
+    f32 = torch.float32
+    with _running_on(device, stream):
         if cu_seqlens is None:
-            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=q.device)
-        _dev(cu_seqlens, "cu_seqlens", torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError(f"cu_seqlens must have shape (N + 1,), got {tuple(cu_seqlens.shape)}")
+            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=device)
+        elif not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 and cu_seqlens.numel() > 0
+                  and _fits(cu_seqlens, torch.int32, cu_seqlens.shape, device)):
+            _dev(cu_seqlens, "cu_seqlens", torch.int32)
+            raise ValueError(f"cu_seqlens must have shape (N + 1,) on {device}, got {tuple(cu_seqlens.shape)} on "
+                             f"{cu_seqlens.device}")
         N = cu_seqlens.numel() - 1
-        if state_in is not None:
-            _dev(state_in, "state_in", torch.float32); _shape(state_in, "state_in", (N, Hv, dv, dk))
+        if state_in is not None and not (isinstance(state_in, torch.Tensor)
+                                         and _fits(state_in, f32, (N, Hv, dv, dk), device)):
+            _explain(state_in, "state_in", f32, (N, Hv, dv, dk), device)
         if o is None:
-            o = torch.empty(T, Hv, dv, dtype=q.dtype, device=q.device)
-        _dev(o, "o", q.dtype); _shape(o, "o", (T, Hv, dv))
+            o = torch.empty(v.shape, dtype=q.dtype, device=device)
+        elif not (isinstance(o, torch.Tensor) and _fits(o, q.dtype, v.shape, device)):
+            _explain(o, "o", q.dtype, v.shape, device)
         if state_out is None:
-            state_out = torch.empty(N, Hv, dv, dk, dtype=torch.float32, device=q.device)
-        _dev(state_out, "state_out", torch.float32); _shape(state_out, "state_out", (N, Hv, dv, dk))
-        need = linear_prefill_workspace_bytes(N, T, Hv, dk, dv, q.dtype)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if workspace is not None:
-            _dev(workspace, "workspace")
-        _on(q.device, k=k, v=v, g=g, state_in=state_in, cu_seqlens=cu_seqlens, o=o, state_out=state_out,
-            workspace=workspace)
-        _check(lib().gdn_linear_prefill(
+            state_out = torch.empty((N, Hv, dv, dk), dtype=f32, device=device)
+        elif not (isinstance(state_out, torch.Tensor) and _fits(state_out, f32, (N, Hv, dv, dk), device)):
+            _explain(state_out, "state_out", f32, (N, Hv, dv, dk), device)
+        if workspace is None:
+            need = _fn("gdn_linear_prefill_workspace_bytes")(N, T, Hv, dk, dv, code)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        elif _dev(workspace, "workspace").device != device:
+            raise ValueError(f"workspace must be on {device}, is on {workspace.device}")
+        _check(_fn("gdn_linear_prefill")(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride,
-            state_in.data_ptr() if state_in is not None else None, cu_seqlens.data_ptr(),
-            N, T, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), state_out.data_ptr(),
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            torch.cuda.current_stream().cuda_stream))
+            None if state_in is None else state_in.data_ptr(), cu_seqlens.data_ptr(),
+            N, T, Hqk, Hv, dk, dv, scale or 0.0, code, o.data_ptr(), state_out.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+            _raw_stream(device)))
     return o, state_out
 
 
@@ -373,24 +409,21 @@ def linear_decode(q, k, v, g, state, *, scale=None, o=None, stream=None):
     """One step of decayed linear attention: q, k [B, Hqk, dk]; v [B, Hv, dv]; g
     [B, Hv] or [Hv]; state [B, Hv, dv, dk] updated in place -- fp32
     (gdn_linear_decode) or bf16 (gdn_linear_decode_bf16_state). Returns o [B, Hv, dv]."""
-    _dev(q, "q"); _dev(k, "k", q.dtype); _dev(v, "v", q.dtype); _dev(state, "state")
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k must be [B, Hqk, dk] and v [B, Hv, dv]")
-    dtype = _dtype_code(q)
-    if state.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"state must be fp32 or bf16, got {state.dtype}")
-    B, Hqk, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[2]
-    _shape(k, "k", (B, Hqk, dk)); _shape(v, "v", (B, Hv, dv)); _shape(state, "state", (B, Hv, dv, dk))
-    g_stride = _decay(g, B, Hv)
-    with _running_on(q.device, stream):
+    device, code, B, Hqk, dk, Hv, dv = _qkv(q, k, v, "B")
+    g_stride = _decay(g, B, Hv, device)
+    sdt = state.dtype if isinstance(state, torch.Tensor) else None
+    if sdt != torch.float32 and sdt != torch.bfloat16:
+        raise TypeError(f"state must be an fp32 or bf16 tensor, got {sdt or type(state).__name__}")
+    if not _fits(state, sdt, (B, Hv, dv, dk), device):
+        _explain(state, "state", sdt, (B, Hv, dv, dk), device)
+    with _running_on(device, stream):
         if o is None:
-            o = torch.empty(B, Hv, dv, dtype=q.dtype, device=q.device)
-        _dev(o, "o", q.dtype); _shape(o, "o", (B, Hv, dv))
-        _on(q.device, k=k, v=v, g=g, state=state, o=o)
-        fn = lib().gdn_linear_decode if state.dtype == torch.float32 else lib().gdn_linear_decode_bf16_state
-        _check(fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride, state.data_ptr(),
-                  B, Hqk, Hv, dk, dv, float(scale or 0.0), dtype, o.data_ptr(), torch.cuda.current_stream().cuda_stream))
+            o = torch.empty(v.shape, dtype=q.dtype, device=device)
+        elif not (isinstance(o, torch.Tensor) and _fits(o, q.dtype, v.shape, device)):
+            _explain(o, "o", q.dtype, v.shape, device)
+        _check(_fn("gdn_linear_decode" if sdt == torch.float32 else "gdn_linear_decode_bf16_state")(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride, state.data_ptr(),
+            B, Hqk, Hv, dk, dv, scale or 0.0, code, o.data_ptr(), _raw_stream(device)))
     return o
 
 
@@ -407,20 +440,33 @@ def state_pool(n_slots, Hv, dv, dk, *, dtype=torch.float8_e4m3fn, device="cuda")
     return codes, torch.zeros(n_slots, Hv, dv, dk // min(32, dk), dtype=torch.uint8, device=device)
 
 
-def _pool_args(codes, exps, slots, state):
-    _dev(codes, "codes"); _dev(exps, "exps", torch.uint8); _dev(slots, "slots", torch.int32); _dev(state, "state")
-    if codes.dtype not in _CODES:
+def _pool_args(codes, exps, slots):
+    """Checks a pool and slot numbers; (device, n, n_slots, Hv, dk, dv, code)."""
+    code = _CODES.get(codes.dtype) if isinstance(codes, torch.Tensor) else None
+    if code is None or not codes.is_cuda or not codes.is_contiguous():
+        _dev(codes, "codes")
         raise TypeError(f"codes must be float8_e4m3fn or int8, got {codes.dtype}")
-    if codes.dim() != 4 or slots.dim() != 1:
-        raise ValueError("codes must be [n_slots, Hv, dv, dk] and slots [n]")
-    if state.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"state must be fp32 or bf16, got {state.dtype}")
+    device = codes.device
+    if codes.dim() != 4:
+        raise ValueError(f"codes must be [n_slots, Hv, dv, dk], got {tuple(codes.shape)}")
     n_slots, Hv, dv, dk = codes.shape
-    n = slots.numel()
-    _shape(exps, "exps", (n_slots, Hv, dv, dk // min(32, dk) if dk else 0))
-    _shape(state, "state", (n, Hv, dv, dk))
-    _on(codes.device, exps=exps, slots=slots, state=state)
-    return n, n_slots, Hv, dk, dv, _CODES[codes.dtype], GDN_F32 if state.dtype == torch.float32 else GDN_BF16
+    want = (n_slots, Hv, dv, dk // min(32, dk) if dk else 0)
+    if not (isinstance(exps, torch.Tensor) and _fits(exps, torch.uint8, want, device)):
+        _explain(exps, "exps", torch.uint8, want, device)
+    if not (isinstance(slots, torch.Tensor) and slots.dim() == 1
+            and _fits(slots, torch.int32, slots.shape, device)):
+        _dev(slots, "slots", torch.int32)
+        raise ValueError(f"slots must have shape (n,) on {device}, got {tuple(slots.shape)} on {slots.device}")
+    return device, slots.shape[0], n_slots, Hv, dk, dv, code
+
+
+def _pool_state(state, shape, device):
+    sdt = state.dtype if isinstance(state, torch.Tensor) else None
+    if sdt != torch.float32 and sdt != torch.bfloat16:
+        raise TypeError(f"state must be an fp32 or bf16 tensor, got {sdt or type(state).__name__}")
+    if not _fits(state, sdt, shape, device):
+        _explain(state, "state", sdt, shape, device)
+    return GDN_F32 if sdt == torch.float32 else GDN_BF16
 
 
 def state_store(state, codes, exps, slots, *, stream=None) -> None:
@@ -428,21 +474,22 @@ def state_store(state, codes, exps, slots, *, stream=None) -> None:
     the pool: value = code 2^(exp - 127), one exponent byte for each 32 values
     along dk. A slot outside the pool is passed over; of several states for one
     slot the last is kept."""
-    n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
-    with _running_on(codes.device, stream):
-        _check(lib().gdn_state_store(state.data_ptr(), sdt, slots.data_ptr(), n, n_slots, Hv, dk, dv, code,
-                                     codes.data_ptr(), exps.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    device, n, n_slots, Hv, dk, dv, code = _pool_args(codes, exps, slots)
+    sdt = _pool_state(state, (n, Hv, dv, dk), device)
+    with _running_on(device, stream):
+        _check(_fn("gdn_state_store")(state.data_ptr(), sdt, slots.data_ptr(), n, n_slots, Hv, dk, dv, code,
+                                      codes.data_ptr(), exps.data_ptr(), _raw_stream(device)))
 
 
 def state_load(codes, exps, slots, *, state=None, dtype=torch.float32, stream=None):
     """Reads slots [n] int32 of the pool into state [n, Hv, dv, dk] (fp32 or bf16;
     allocated as `dtype` if not given) and returns it. A slot outside the pool
     gives a zero state."""
-    _dev(codes, "codes"); _dev(slots, "slots", torch.int32)
-    with _running_on(codes.device, stream):
+    device, n, n_slots, Hv, dk, dv, code = _pool_args(codes, exps, slots)
+    with _running_on(device, stream):
         if state is None:
-            state = torch.empty(slots.numel(), *codes.shape[1:], dtype=dtype, device=codes.device)
-        n, n_slots, Hv, dk, dv, code, sdt = _pool_args(codes, exps, slots, state)
-        _check(lib().gdn_state_load(codes.data_ptr(), exps.data_ptr(), slots.data_ptr(), n, n_slots, Hv, dk, dv,
-                                    code, state.data_ptr(), sdt, torch.cuda.current_stream().cuda_stream))
+            state = torch.empty((n, Hv, dv, dk), dtype=dtype, device=device)
+        sdt = _pool_state(state, (n, Hv, dv, dk), device)
+        _check(_fn("gdn_state_load")(codes.data_ptr(), exps.data_ptr(), slots.data_ptr(), n, n_slots, Hv, dk, dv, code,
+                                     state.data_ptr(), sdt, _raw_stream(device)))
     return state
