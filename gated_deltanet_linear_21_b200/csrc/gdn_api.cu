@@ -451,17 +451,19 @@ gdn_status linear_decode(const char* fn, const void* q, const void* k, const voi
   if (gdn_status s = check_decode(fn, q, k, v, g, g, state, B, Hqk, Hv, dk, dv, dtype, o, &done)) return s;
   if (g_stride != 0 && g_stride != Hv)
     return fail(GDN_ERR_INVALID_ARG, "%s: g_stride=%d (0 or Hv=%d)", fn, g_stride, Hv);
+  if ((int64_t)B * Hv * 8 > 0x7fffffff) return fail(GDN_ERR_INVALID_ARG, "%s: B*Hv too large", fn);   // (8 CTAs a head at most)
   if (done) return ok();
   if (scale <= 0.f) scale = 1.0f / sqrtf((float)dk);
   return with_dtype(dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
     return with_dk(dk, [&](auto dkc) {
       constexpr int DK = decltype(dkc)::value;
-      using Sh = gdn::DecodeShape<DK, TS>;
-      const dim3 grid((unsigned)(B * Hv), (unsigned)((dv + Sh::kRowsPerCta - 1) / Sh::kRowsPerCta));
-      gdn::lin::decode_kernel<T, DK, TS><<<grid, Sh::kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
-          static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_stride, state, Hqk, Hv,
-          dv, scale, static_cast<T*>(o));
+      constexpr int kRows = gdn::lin::LinearDecodeShape<DK, TS>::kRowsPerCta;
+      const int parts = (dv + kRows - 1) / kRows;
+      gdn::lin::decode_kernel<T, DK, TS>
+          <<<(unsigned)(B * Hv) * parts, gdn::lin::kDecodeWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+              static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_stride, state, Hqk, Hv,
+              dv, parts, scale, static_cast<T*>(o));
       return launch_status(fn);
     });
   });
