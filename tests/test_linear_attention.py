@@ -233,6 +233,98 @@ def test_two_calls_at_once():
     gdn.device_error()
 
 
+# ------------------------------------------- prefill, split over time and heads ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("lengths,Hqk,Hv,dk,dv", [
+    ([1300], 2, 20, 128, 128),                                  # more heads than one turn of the scan takes
+    ([2600, 0, 1, 1500], 19, 38, 16, 32),
+    ([0] * 3 + [1] * 40 + [1700] + [3] * 40 + [0] * 5 + [900], 2, 4, 64, 128),
+    ([1500, 1100], 1, 1, 32, 16)], ids=["20 heads", "38 heads", "short around long", "one head"])
+def test_prefill_split_over_time(dtype, lengths, Hqk, Hv, dk, dv):
+    x = draw(lengths, Hqk, Hv, dk, dv, dtype, seed=50)
+    check(x, *prefill(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("kind", ["strong", "reset", "far", "positive"])
+def test_prefill_decays_across_segments(dtype, kind):
+    x = draw([2300], 1, 2, 32, 64, dtype, kind, seed=51)
+    if kind == "positive":      # 2300 tokens that grow would leave the range
+        x["g"][300:] = 0.0
+    check(x, *prefill(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_a_reset_and_bad_neighbours_across_segments(dtype):
+    """A sequence of NaN that is split over time leaves the one behind it alone."""
+    x = draw([1300, 1100], 1, 2, 64, 64, dtype, seed=52)
+    want = {n: t.clone() for n, t in x.items()}
+    x["k"][40:1290] = float("nan")
+    x["state_in"][0] = float("inf")
+    o, s = prefill(x)
+    assert torch.isnan(o[1299]).all() and torch.isnan(s[0]).any()
+    ro, rs, mo, ms = ref.linear_prefill(*(want[n] for n in ("q", "k", "v", "g", "state_in", "cu")))
+    ref.check_o(o[1300:], ro[1300:], mo[1300:], 1100, 64)
+    ref.check_state(s[1], rs[1], ms[1], 1100)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_two_graphs_that_share_a_workspace_replayed_in_turn(dtype):
+    xs = [on_gpu(draw(n, 2, 4, 128, 128, dtype, seed=53)) for n in ([1900, 30], [700, 1400])]
+    args = lambda x: (x["q"], x["k"], x["v"], x["g"], x["state_in"], x["cu"])  # noqa: E731
+    want = [gdn.linear_prefill(*args(x)) for x in xs]
+    need = max(gdn.linear_prefill_workspace_bytes(2, x["q"].shape[0], 4, 128, 128, dtype) for x in xs)
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)     # its contents do not matter
+    graphs, outs = [], []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(gdn.linear_prefill(*args(x), workspace=ws))
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 1):
+        outs[i][0].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+    gdn.device_error()
+
+
+@pytest.mark.gpu
+def test_prefill_and_decode_beyond_32_bit_offsets():
+    """v, o and the states have more than 2^31 elements; what lies behind them is checked."""
+    T, tail, Hv, dk, dv = 131085, 300, 128, 16, 128
+    small = draw([tail], 1, Hv, dk, dv, BF16, seed=54)
+    d = on_gpu(small)
+    q, k = (torch.zeros(T + tail, 1, dk, dtype=BF16, device=DEV) for _ in range(2))
+    v, g = torch.zeros(T + tail, Hv, dv, dtype=BF16, device=DEV), torch.zeros(T + tail, Hv, device=DEV)
+    for big, n in ((q, "q"), (k, "k"), (v, "v"), (g, "g")):
+        big[T:] = d[n]
+    state = torch.zeros(2, Hv, dv, dk, device=DEV)
+    state[1] = d["state_in"][0]
+    cu = torch.tensor([0, T, T + tail], dtype=torch.int32, device=DEV)
+    assert v.numel() > 2 ** 31
+    o, s = gdn.linear_prefill(q, k, v, g, state, cu)
+    gdn.device_error()
+    check(small, o[T:], s[1:])
+    assert not o[T - 200:T].any() and not s[0].any()
+    del v, o, q, k
+    B, dk = 1030, 128
+    y = on_gpu(draw([1], 1, Hv, dk, dv, BF16, seed=55))
+    want_s = y["state_in"].clone()
+    want_o = gdn.linear_decode(y["q"], y["k"], y["v"], y["g"], want_s)
+    many = {n: y[n].expand(B, *y[n].shape[1:]).contiguous() for n in ("q", "k", "v", "g", "state_in")}
+    assert many["state_in"].numel() > 2 ** 31
+    o = gdn.linear_decode(many["q"], many["k"], many["v"], many["g"], many["state_in"])
+    for b in (0, 1023, 1024, B - 1):
+        assert torch.equal(o[b], want_o[0]) and torch.equal(many["state_in"][b], want_s[0])
+
+
 # ------------------------------------------------------------------ decode ---
 
 def decode_reference(x, state, scale=None):
@@ -346,6 +438,19 @@ INV, UNS = gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_UNSUPPORTED
 def test_prefill_refuses(lib, kw, status):
     assert _c_prefill(lib, **kw) == status
     assert lib.gdn_last_error().decode().startswith("gdn_linear_prefill")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_prefill_workspace_is_checked(lib, dtype):
+    code = {BF16: gdn.GDN_BF16, F16: gdn.GDN_F16, F32: gdn.GDN_F32}[dtype]
+    need = gdn.linear_prefill_workspace_bytes(1, 4096, 4, 128, 128, dtype)
+    assert need > 0
+    assert gdn.linear_prefill_workspace_bytes(1, 1, 4, 128, 128, dtype) == 0
+    assert gdn.linear_prefill_workspace_bytes(0, 4096, 4, 128, 128, dtype) == 0
+    assert gdn.linear_prefill_workspace_bytes(3, 0, 4, 128, 128, dtype) == 0
+    for kw in (dict(ws=None), dict(ws_bytes=need - 1), dict(ws=P + 8), dict(ws=P, ws_bytes=0)):
+        assert _c_prefill(lib, dtype=code, total_T=4096, **{"ws_bytes": need, **kw}) == INV
+        assert "workspace" in lib.gdn_last_error().decode()
 
 
 @pytest.mark.parametrize("name", ["gdn_linear_decode", "gdn_linear_decode_bf16_state"])

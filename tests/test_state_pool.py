@@ -163,6 +163,20 @@ def test_an_empty_pool_and_no_states():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("code", CODES)
+def test_a_pool_beyond_32_bit_offsets(code):
+    slots, Hv, d = 1030, 128, 128
+    x = states(2, Hv, d, d, F32, seed=10)
+    codes, exps = gdn.state_pool(slots, Hv, d, d, dtype=code)
+    assert codes.numel() > 2 ** 31
+    slot = torch.tensor([slots - 1, 1023], dtype=torch.int32, device=DEV)
+    gdn.state_store(x.to(DEV), codes, exps, slot)
+    assert same(ref.f64(gdn.state_load(codes, exps, slot)), ref.quantise(x, code)[0])
+    near = torch.tensor([0, 1022, 1024, slots - 2], dtype=torch.int32, device=DEV)
+    assert not gdn.state_load(codes, exps, near).any()
+
+
+@pytest.mark.gpu
 def test_captured_and_on_another_stream():
     x = states(4, 2, 128, 128, F32, seed=6).to(DEV)
     codes, exps = gdn.state_pool(6, 2, 128, 128)
