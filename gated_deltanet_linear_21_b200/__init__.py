@@ -436,6 +436,8 @@ def state_pool(n_slots, Hv, dv, dk, *, dtype=torch.float8_e4m3fn, device="cuda")
     zero states: a pool for state_store and state_load, in float8_e4m3fn or int8."""
     if dtype not in _CODES:
         raise TypeError(f"codes must be float8_e4m3fn or int8, got {dtype}")
+    if dk not in (16, 32, 64, 128) or dv not in (16, 32, 64, 128):
+        raise ValueError(f"dk={dk}, dv={dv} (supported: 16, 32, 64, 128)")
     codes = torch.zeros(n_slots, Hv, dv, dk, dtype=torch.int8, device=device).view(dtype)
     return codes, torch.zeros(n_slots, Hv, dv, dk // min(32, dk), dtype=torch.uint8, device=device)
 

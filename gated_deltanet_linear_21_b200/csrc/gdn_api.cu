@@ -592,6 +592,7 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
   prm.Hv = Hv;
   prm.dv = dv;
   prm.seg = plan.seg;
+  prm.segments = (int)plan.segments;
   prm.scale = scale;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_dk(dk, [&](auto dkc) {

@@ -132,6 +132,7 @@ struct ScanParams {
   float* states;       // [segments][Hv][dv][dk]: each segment's own state, then the one that enters it
   float* decays;       // [segments][Hv]
   int g_stride, n_seqs, total_T, Hqk, Hv, dv, seg;
+  int segments;        // that the workspace has room for
   float scale;
 };
 
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(256)
 combine_kernel(const ScanParams p, int per_state) {
   const int h = blockIdx.y, n = blockIdx.z, at = (blockIdx.x * 256 + threadIdx.x) * 4, lane = threadIdx.x & 31;
   // the sequence's first segment: those of the sequences before it
-  int first = 0, J = 0;
+  long long first = 0;
+  int J = 0;
   for (int m = 0; m <= n; m += 32) {
     int x = 0;
     if (m + lane <= n) {
@@ -296,6 +298,7 @@ combine_kernel(const ScanParams p, int per_state) {
   J = __reduce_max_sync(0xffffffffu, J);
   first -= J;
   if (J == 1 || at >= per_state) return;
+  if (first + J > p.segments) return;   // (sequences that overlap, which no valid cu_seqlens makes)
   const size_t own = ((size_t)n * p.Hv + h) * per_state + at, step = (size_t)p.Hv * per_state;
   float* slot = p.states + ((size_t)first * p.Hv + h) * per_state + at;
   const float* decay = p.decays + (size_t)first * p.Hv + h;

@@ -284,7 +284,10 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  *              g_stride = 0 (one fixed for each value head). -infinity is a
  *              reset: the state before that token counts for nothing from it on.
  *   state_in   [n_seqs, Hv, dv, dk]  fp32, or NULL for zero states
- *   cu_seqlens [n_seqs + 1] int32, as gdn_prefill's
+ *   cu_seqlens [n_seqs + 1] int32, read on the device. Non-decreasing, inside
+ *              [0, total_T]; it may begin behind 0 and end before total_T. One
+ *              that breaks this is not detected: nothing outside the arrays is
+ *              read or written, and the outputs are not defined.
  *   o          [total_T, Hv, dv]     dtype (output); rows before the first
  *              sequence and behind the last are left as they were
  *   state_out  [n_seqs, Hv, dv, dk]  fp32 (output); may be state_in. A sequence
@@ -293,8 +296,15 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  *              contents on entry do not matter). Calls that may overlap on the
  *              GPU, captured graphs among them, need workspaces of their own.
  *
+ * o overlaps none of the inputs. scale <= 0 stands for dk^-1/2. Infinities and
+ * NaN in a sequence's q, k, v or state_in stay within that sequence, but may
+ * reach rows of o up to 127 tokens before the one that holds them. A bounded
+ * wait that ran out is reported by gdn_device_error.
+ *
  * Supported: every dtype, dk and dv in {16, 32, 64, 128}; n_seqs and Hv up to
- * 65535. State and sums are fp32.
+ * 65535. State and sums are fp32. For bf16 and f16 the state that meets q and
+ * the decayed scores are rounded to the input type (o holds no more); the state
+ * that is carried is not, and repeated calls give the same bits.
  */
 size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype);
 gdn_status gdn_linear_prefill(const void *q, const void *k, const void *v,

@@ -189,6 +189,22 @@ def test_a_broken_cu_seqlens_reads_and_writes_nothing_outside():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cu", [[0, 4000, 0, 4000, 0, 4000], [0, 0, 4000, 10, 3990, -7, 5000]], ids=str)
+def test_sequences_that_overlap_leave_what_is_behind_the_workspace(dtype, cu):
+    """Offsets that go back make more segments than the workspace has room for."""
+    x = draw([4000], 1, 2, 64, 64, dtype, init=False, seed=13)
+    d, n = on_gpu(x), len(cu) - 1
+    need = gdn.linear_prefill_workspace_bytes(n, 4000, 2, 64, 64, dtype)
+    assert need > 0 and need % 16 == 0
+    ws = torch.full((need + (64 << 20),), 171, dtype=torch.uint8, device=DEV)
+    gdn.linear_prefill(d["q"], d["k"], d["v"], d["g"], None, torch.tensor(cu, dtype=torch.int32, device=DEV),
+                       workspace=ws[:need])
+    gdn.device_error()
+    assert (ws[need:] == 171).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_repeated_captured_and_on_another_stream(dtype):
     x = draw([900, 130, 1], 2, 4, 128, 128, dtype, seed=11)
     o, s = prefill(x)
@@ -244,6 +260,14 @@ def test_two_calls_at_once():
     ([1500, 1100], 1, 1, 32, 16)], ids=["20 heads", "38 heads", "short around long", "one head"])
 def test_prefill_split_over_time(dtype, lengths, Hqk, Hv, dk, dv):
     x = draw(lengths, Hqk, Hv, dk, dv, dtype, seed=50)
+    check(x, *prefill(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_many_short_sequences(dtype):
+    lengths = torch.randint(0, 4, (2500,), generator=torch.Generator().manual_seed(54)).tolist()
+    x = draw(lengths, 1, 2, 16, 32, dtype, seed=54)
     check(x, *prefill(x))
 
 

@@ -290,6 +290,9 @@ def test_no_states_is_a_no_op(lib):
 def test_the_binding_refuses():
     with pytest.raises(TypeError):
         gdn.state_pool(2, 2, 16, 16, dtype=torch.uint8, device="cpu")
+    for dv, dk in ((16, 0), (16, 96), (256, 16)):
+        with pytest.raises(ValueError):
+            gdn.state_pool(2, 2, dv, dk, device="cpu")
     codes, exps = gdn.state_pool(2, 2, 16, 16, device="cpu")
     with pytest.raises(TypeError):
         gdn.state_store(torch.zeros(1, 2, 16, 16), codes, exps, torch.zeros(1, dtype=torch.int32))
