@@ -384,9 +384,13 @@ int linear_segment(int n_seqs, int64_t total_T, int Hv) {
   return (int)std::min<int64_t>(8, std::max<int64_t>(1, (blocks + kLinearCtas - 1) / kLinearCtas));
 }
 
-// fp32: tokens per segment, so that about 2400 CTAs of one segment's 32 state rows each
-// are at work, and the workspace of the segments' states: what precedes the states holds
-// their decays.
+// fp32: tokens per segment, and the workspace of the segments' states (what precedes the
+// states holds their decays). Splitting costs a second pass over k and v. Where the
+// sequences' heads fill the GPU by themselves only those of twice the mean length are
+// split (16 x 300 tokens, 32 heads of 128: 425 us, in segments for four waves 692); where a
+// wave of resident CTAs holds two segments of each sequence or more, all of them are in one
+// wave (3300 tokens, 16 heads of 64: 85 us, 102 with the last tenth in a second one); in
+// between, in about four.
 struct ScanPlan {
   int seg;
   int64_t segments;    // at most
@@ -394,9 +398,12 @@ struct ScanPlan {
 };
 ScanPlan scan_plan(int n_seqs, int64_t total_T, int Hv, int dk, int dv) {
   ScanPlan s;
-  const int64_t rows = (dv + gdn::lin::kScanRows - 1) / gdn::lin::kScanRows;
-  const int64_t blocks = (total_T * Hv * rows / 2400 + 63) / 64;
-  s.seg = (int)(64 * std::max<int64_t>(1, blocks));
+  const int64_t rows = (dv + gdn::lin::scan_rows(dv) - 1) / gdn::lin::scan_rows(dv);
+  const int64_t resident = 148 * (dk == 128 ? 4 : 5), per_wave = resident / (Hv * rows);
+  const int64_t want = per_wave > 2 * n_seqs ? per_wave - n_seqs
+                       : per_wave > n_seqs   ? 4 * resident / (Hv * rows)
+                                             : std::max(1, n_seqs / 2);
+  s.seg = (int)std::min<int64_t>(std::max<int64_t>(64, (total_T / want + 16) / 16 * 16), 1 << 30);
   s.segments = total_T / s.seg + n_seqs;
   s.decay_bytes = ((size_t)s.segments * Hv * 4 + 255) & ~size_t(255);
   s.bytes = total_T <= s.seg ? 0 : s.decay_bytes + (size_t)s.segments * Hv * dv * dk * 4;
@@ -595,20 +602,24 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
   prm.segments = (int)plan.segments;
   prm.scale = scale;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return with_dk(dk, [&](auto dkc) {
-    constexpr int DK = decltype(dkc)::value;
-    const dim3 grid((unsigned)plan.segments, (unsigned)Hv, (unsigned)((dv + gdn::lin::kScanRows - 1) / gdn::lin::kScanRows));
+  auto run = [&](auto dkc, auto rows) {
+    constexpr int DK = decltype(dkc)::value, R = decltype(rows)::value;
+    const dim3 grid((unsigned)plan.segments, (unsigned)Hv, (unsigned)((dv + 32 * R - 1) / (32 * R)));
     const auto *qf = static_cast<const float*>(q), *kf = static_cast<const float*>(k), *vf = static_cast<const float*>(v);
     auto* of = static_cast<float*>(o);
     if (need > 0) {
-      gdn::lin::scan_kernel<float, DK, false><<<grid, gdn::lin::kScanThreads, 0, st>>>(qf, kf, vf, of, prm);
+      gdn::lin::scan_kernel<DK, R, false><<<grid, gdn::lin::kScanThreads, 0, st>>>(qf, kf, vf, of, prm);
       if (gdn_status s = launch_status(fn)) return s;
       gdn::lin::combine_kernel<<<dim3((unsigned)((dv * DK + 1023) / 1024), (unsigned)Hv, (unsigned)n_seqs), 256, 0, st>>>(
           prm, dv * DK);
       if (gdn_status s = launch_status(fn)) return s;
     }
-    gdn::lin::scan_kernel<float, DK, true><<<grid, gdn::lin::kScanThreads, 0, st>>>(qf, kf, vf, of, prm);
+    gdn::lin::scan_kernel<DK, R, true><<<grid, gdn::lin::kScanThreads, 0, st>>>(qf, kf, vf, of, prm);
     return launch_status(fn);
+  };
+  return with_dk(dk, [&](auto dkc) {
+    return gdn::lin::scan_rows_per_lane(dv) == 2 ? run(dkc, std::integral_constant<int, 2>())
+                                                 : run(dkc, std::integral_constant<int, 1>());
   });
 }
 

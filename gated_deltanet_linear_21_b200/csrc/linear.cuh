@@ -106,9 +106,12 @@ decode_kernel(const TIO* __restrict__ q, const TIO* __restrict__ k, const TIO* _
 // --------------------------------------------------------------- prefill ---
 // The recurrence token by token in fp32, for fp32 inputs (the tensor cores' products
 // would round them). A state row is spread over 4 lanes (columns 4 (sub + 4 i) .. + 3), 8
-// rows a warp, and stays in registers; a block of 16 tokens' q, k and v is staged in
-// shared memory, where the 8 row groups of a warp read the same q and k words. Issue
-// bound: three operations a state element and token, two in the first pass.
+// rows a warp, and stays in registers; blocks of 16 tokens' q, k and v are staged in
+// shared memory, one ahead, where the 8 row groups of a warp read the same q and k words.
+// Those reads are what bounds it, before the arithmetic (three operations a state element
+// and token where o is made, one in the first pass), so a lane holds two rows where d_v
+// has them: one 4096-token sequence of 16 heads of 128 takes 300 us, 32 packed heads of
+// 16 x 300 tokens 425 us; with one row a lane and no stage ahead 477 and 1218.
 //
 // Over time. Heads and rows alone give few warps, each with one long chain, so sequences
 // are cut into segments of `seg` tokens, all worked on at once, in three launches: each
@@ -117,12 +120,23 @@ decode_kernel(const TIO* __restrict__ q, const TIO* __restrict__ k, const TIO* _
 //
 // Precision. exp(g_t) rounded once is off by up to 2^-24, always the same way where the
 // decay is fixed, which a thousand tokens add up to 6e-5. So the decays that are carried
-// far are exact: across segments exp of the sum of g in fp64, and inside one the state
-// is corrected after every block of 16 tokens by exp of the block's sum over the product
+// far are exact: across segments and, in the first pass, across blocks of 16 tokens exp of
+// sums of g in fp64 (a token enters with the weight it has at its block's end); where o is
+// made the state is corrected after every block by exp of the block's sum over the product
 // of the rounded decays.
 constexpr int kScanTokens = 16;   // tokens staged at a time
-constexpr int kScanRows = 32;     // state rows per CTA: 4 warps of 8
 constexpr int kScanThreads = 128;
+// State rows per lane, and of a CTA of 4 warps.
+__host__ __device__ constexpr int scan_rows_per_lane(int dv) { return dv >= 64 ? 2 : 1; }
+__host__ __device__ constexpr int scan_rows(int dv) { return 32 * scan_rows_per_lane(dv); }
+
+// 16 bytes to shared memory, of which the first `bytes` are read and the others zeros.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 struct ScanParams {
   const float* g;
@@ -172,17 +186,19 @@ __device__ __forceinline__ bool find_segment(const ScanParams& p, int item, Segm
   return false;
 }
 
-// grid: (segments at most, Hv, ceil(dv / kScanRows))
-template <typename TIO, int DK, bool kOut>
+// grid: (segments at most, Hv, ceil(dv / (32 kR)))
+template <int DK, int kR, bool kOut>
 __global__ void __launch_bounds__(kScanThreads)
-scan_kernel(const TIO* __restrict__ q, const TIO* __restrict__ k, const TIO* __restrict__ v, TIO* __restrict__ o,
+scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v, float* __restrict__ o,
             const ScanParams p) {
   constexpr int E = DK / 4;                  // columns per lane
-  __shared__ __align__(16) float qs[kOut ? kScanTokens : 1][DK];
-  __shared__ __align__(16) float ks[kScanTokens][DK];
-  __shared__ float vs[kScanTokens][kScanRows];   // v, replaced by o
-  __shared__ float as[kScanTokens];
-  __shared__ float fix;
+  constexpr int kScanRows = 32 * kR;
+  // two stages: the next one's tokens arrive while this one's are worked on
+  __shared__ __align__(16) float qs[2][kOut ? kScanTokens : 1][DK];
+  __shared__ __align__(16) float ks[2][kScanTokens][DK];
+  __shared__ __align__(16) float vs[2][kScanTokens][kScanRows];   // v, replaced by o
+  __shared__ float as[2][kScanTokens];       // kOut: exp(g); else the weight of a token in the state behind the stage
+  __shared__ float fix[2];                   // kOut: what the product of the exp(g) is corrected by; else the stage's decay
   const int h = blockIdx.y, hq = h / (p.Hv / p.Hqk), dv = p.dv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane & 3, rl = warp * 8 + (lane >> 2);
@@ -191,94 +207,162 @@ scan_kernel(const TIO* __restrict__ q, const TIO* __restrict__ k, const TIO* __r
   if (!find_segment(p, blockIdx.x, it)) return;
   if (!kOut && it.J == 1) return;            // nothing to combine
 
+  // row 32 u further on: u * 32 * DK words
   const size_t slot = (((size_t)blockIdx.x * p.Hv + h) * dv + row) * DK + 4 * sub;
   const size_t srow = (((size_t)it.n * p.Hv + h) * dv + row) * DK + 4 * sub;
   const float* from = !kOut ? nullptr : it.J > 1 ? p.states + slot : p.state_in ? p.state_in + srow : nullptr;
-  float s[E];
+  float s[kR][E];
 #pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    const float4 x = from && row < dv ? *reinterpret_cast<const float4*>(from + 16 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    s[4 * i] = x.x; s[4 * i + 1] = x.y; s[4 * i + 2] = x.z; s[4 * i + 3] = x.w;
+  for (int u = 0; u < kR; ++u) {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const float4 x = from && row + 32 * u < dv ? *reinterpret_cast<const float4*>(from + 32 * u * DK + 16 * i)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      s[u][4 * i] = x.x; s[u][4 * i + 1] = x.y; s[u][4 * i + 2] = x.z; s[u][4 * i + 3] = x.w;
+    }
   }
 
   double sum = 0.0;                          // of the segment's g (warp 0)
-  for (int c0 = 0; c0 < it.len; c0 += kScanTokens) {
-    const int L = min(kScanTokens, it.len - c0), t0 = it.t0 + c0;
+  auto fetch = [&](int c0) {
+    const int L = min(kScanTokens, it.len - c0), t0 = it.t0 + c0, b = (c0 / kScanTokens) & 1;
     for (int e = tid; e < L * (DK / 4); e += kScanThreads) {
       const int t = e / (DK / 4), j = 4 * (e - t * (DK / 4));
       const size_t at = ((size_t)(t0 + t) * p.Hqk + hq) * DK + j;
-      if constexpr (kOut) {
-        float4 x = load4(q + at);
-        x.x *= p.scale; x.y *= p.scale; x.z *= p.scale; x.w *= p.scale;
-        *reinterpret_cast<float4*>(&qs[t][j]) = x;
-      }
-      *reinterpret_cast<float4*>(&ks[t][j]) = load4(k + at);
+      if constexpr (kOut) copy16_async(&qs[b][t][j], q + at, 16);
+      copy16_async(&ks[b][t][j], k + at, 16);
     }
-    for (int e = tid; e < L * kScanRows; e += kScanThreads) {
-      const int t = e / kScanRows, i = e - t * kScanRows;
-      vs[t][i] = i0 + i < dv ? to_f32(v[((size_t)(t0 + t) * p.Hv + h) * dv + i0 + i]) : 0.f;
+    for (int e = tid; e < L * (kScanRows / 4); e += kScanThreads) {
+      const int t = e / (kScanRows / 4), i = 4 * (e - t * (kScanRows / 4));
+      const bool in = i0 + i < dv;           // (zeros behind the last row)
+      copy16_async(&vs[b][t][i], v + ((size_t)(t0 + t) * p.Hv + h) * dv + (in ? i0 + i : 0), in ? 16 : 0);
     }
-    if (warp == 0) {
-      const float g = lane < L ? p.g[(size_t)(t0 + lane) * p.g_stride + h] : 0.f;
-      const float a = expf(g);
-      if (lane < L) as[lane] = a;
-      double gs = g, prod = lane < L ? (double)a : 1.0;
+  };
+  // by warp 0
+  auto gate = [&](int c0) {
+    return lane < min(kScanTokens, it.len - c0) ? p.g[(size_t)(it.t0 + c0 + lane) * p.g_stride + h] : 0.f;
+  };
+  auto decays = [&](int c0, float g) {
+    const int b = (c0 / kScanTokens) & 1;
+    if constexpr (kOut) {
+      const float a = expf(g);               // (1 behind the last token)
+      if (lane < kScanTokens) as[b][lane] = a;
+      double gs = g, prod = a;
 #pragma unroll
       for (int off = kScanTokens / 2; off > 0; off >>= 1) {
         gs += __shfl_xor_sync(0xffffffffu, gs, off);
         prod *= __shfl_xor_sync(0xffffffffu, prod, off);
       }
-      sum += gs;
-      if (lane == 0) fix = prod > 1e-30 ? (float)(exp(gs) / prod) : 1.f;   // (below, nothing is left to correct)
+      if (lane == 0) fix[b] = prod > 1e-30 ? (float)(exp(gs) / prod) : 1.f;   // (below, nothing is left to correct)
+    } else {
+      double after = g;                      // the sum of g from this token to the stage's end, then from the next one
+#pragma unroll
+      for (int off = 1; off < kScanTokens; off <<= 1) {
+        const double x = __shfl_down_sync(0xffffffffu, after, off);
+        if (lane + off < kScanTokens) after += x;
+      }
+      const double all = __shfl_sync(0xffffffffu, after, 0), next = __shfl_down_sync(0xffffffffu, after, 1);
+      const float w = (float)exp(lane == kScanTokens ? all : lane + 1 < kScanTokens ? next : 0.0);
+      if (lane < kScanTokens) as[b][lane] = w;
+      if (lane == kScanTokens) fix[b] = w;
+      sum += all;
     }
-    __syncthreads();
+  };
+  if (it.len > 0) {
+    fetch(0);
+    if (warp == 0) decays(0, gate(0));
+  }
+  for (int c0 = 0; c0 < it.len; c0 += kScanTokens) {
+    const int L = min(kScanTokens, it.len - c0), t0 = it.t0 + c0, b = (c0 / kScanTokens) & 1;
+    const bool more = c0 + kScanTokens < it.len;
+    wait_copies();
+    __syncthreads();                         // this stage is there, and the one before has been left
+    float g_next = 0.f;
+    if (more) {
+      fetch(c0 + kScanTokens);
+      if (warp == 0) g_next = gate(c0 + kScanTokens);
+    }
+    const float f = fix[b];
+    if constexpr (!kOut) {
+#pragma unroll
+      for (int u = 0; u < kR; ++u) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[u][i] *= f;
+      }
+    }
     for (int t = 0; t < L; ++t) {
-      const float a = as[t], vi = vs[t][rl];
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const float a = as[b][t];
+      float vi[kR], acc[kR][4];
+#pragma unroll
+      for (int u = 0; u < kR; ++u) {
+        vi[u] = vs[b][t][rl + 32 * u];
+        if constexpr (!kOut) vi[u] *= a;
+        acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
-        const float4 kk = *reinterpret_cast<const float4*>(&ks[t][4 * (sub + 4 * i)]);
-        s[4 * i] = fmaf(a, s[4 * i], vi * kk.x);
-        s[4 * i + 1] = fmaf(a, s[4 * i + 1], vi * kk.y);
-        s[4 * i + 2] = fmaf(a, s[4 * i + 2], vi * kk.z);
-        s[4 * i + 3] = fmaf(a, s[4 * i + 3], vi * kk.w);
-        if constexpr (kOut) {
-          const float4 qq = *reinterpret_cast<const float4*>(&qs[t][4 * (sub + 4 * i)]);
-          acc[0] = fmaf(s[4 * i], qq.x, acc[0]);
-          acc[1] = fmaf(s[4 * i + 1], qq.y, acc[1]);
-          acc[2] = fmaf(s[4 * i + 2], qq.z, acc[2]);
-          acc[3] = fmaf(s[4 * i + 3], qq.w, acc[3]);
+        const float4 kk = *reinterpret_cast<const float4*>(&ks[b][t][4 * (sub + 4 * i)]);
+        float4 qq;
+        if constexpr (kOut) qq = *reinterpret_cast<const float4*>(&qs[b][t][4 * (sub + 4 * i)]);
+#pragma unroll
+        for (int u = 0; u < kR; ++u) {
+          float* x = s[u] + 4 * i;
+          if constexpr (kOut) {
+            x[0] = fmaf(a, x[0], vi[u] * kk.x);
+            x[1] = fmaf(a, x[1], vi[u] * kk.y);
+            x[2] = fmaf(a, x[2], vi[u] * kk.z);
+            x[3] = fmaf(a, x[3], vi[u] * kk.w);
+            acc[u][0] = fmaf(x[0], qq.x, acc[u][0]);
+            acc[u][1] = fmaf(x[1], qq.y, acc[u][1]);
+            acc[u][2] = fmaf(x[2], qq.z, acc[u][2]);
+            acc[u][3] = fmaf(x[3], qq.w, acc[u][3]);
+          } else {
+            x[0] = fmaf(vi[u], kk.x, x[0]);
+            x[1] = fmaf(vi[u], kk.y, x[1]);
+            x[2] = fmaf(vi[u], kk.z, x[2]);
+            x[3] = fmaf(vi[u], kk.w, x[3]);
+          }
         }
       }
       if constexpr (kOut) {
-        const float r = group_sum<4>((acc[0] + acc[1]) + (acc[2] + acc[3]));
-        if (sub == 0) vs[t][rl] = r;         // only this row's lanes read v_t[row], and they have
+#pragma unroll
+        for (int u = 0; u < kR; ++u) {
+          const float r = group_sum<4>((acc[u][0] + acc[u][1]) + (acc[u][2] + acc[u][3]));
+          if (sub == 0) vs[b][t][rl + 32 * u] = p.scale * r;   // only this row's lanes read v_t[row], and they have
+        }
       }
     }
-    const float f = fix;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s[i] *= f;
-    __syncthreads();
+    if (more && warp == 0) decays(c0 + kScanTokens, g_next);
     if constexpr (kOut) {
-      for (int e = tid; e < L * kScanRows; e += kScanThreads) {
-        const int t = e / kScanRows, i = e - t * kScanRows;
-        if (i0 + i < dv) o[((size_t)(t0 + t) * p.Hv + h) * dv + i0 + i] = from_f32<TIO>(vs[t][i]);
+#pragma unroll
+      for (int u = 0; u < kR; ++u) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[u][i] *= f;
       }
       __syncthreads();
+      for (int e = tid; e < L * (kScanRows / 4); e += kScanThreads) {
+        const int t = e / (kScanRows / 4), i = 4 * (e - t * (kScanRows / 4));
+        if (i0 + i < dv)
+          *reinterpret_cast<float4*>(o + ((size_t)(t0 + t) * p.Hv + h) * dv + i0 + i) =
+              *reinterpret_cast<const float4*>(&vs[b][t][i]);
+      }
     }
   }
   float* to = !kOut ? p.states + slot : it.J == 1 ? p.state_out + srow : nullptr;
-  if (to && row < dv) {
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i)
-      *reinterpret_cast<float4*>(to + 16 * i) = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+  for (int u = 0; u < kR; ++u) {
+    if (to && row + 32 * u < dv) {
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        *reinterpret_cast<float4*>(to + 32 * u * DK + 16 * i) =
+            make_float4(s[u][4 * i], s[u][4 * i + 1], s[u][4 * i + 2], s[u][4 * i + 3]);
+    }
   }
   if (!kOut && i0 == 0 && tid == 0) p.decays[(size_t)blockIdx.x * p.Hv + h] = (float)exp(sum);
 }
 
 // The states that enter the segments, in place of the segments' own, and the final ones.
 // grid: (ceil(dv dk / 1024), Hv, n_seqs); 256 threads of 4 values. Bound by the bytes of the
-// states; four segments' loads are in flight at a time.
+// states; eight segments' loads are in flight at a time.
 __global__ void __launch_bounds__(256)
 combine_kernel(const ScanParams p, int per_state) {
   const int h = blockIdx.y, n = blockIdx.z, at = (blockIdx.x * 256 + threadIdx.x) * 4, lane = threadIdx.x & 31;
@@ -303,24 +387,29 @@ combine_kernel(const ScanParams p, int per_state) {
   float* slot = p.states + ((size_t)first * p.Hv + h) * per_state + at;
   const float* decay = p.decays + (size_t)first * p.Hv + h;
   float4 s = p.state_in ? *reinterpret_cast<const float4*>(p.state_in + own) : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < J; j += 4) {
-    float4 x[4];
-    float a[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (j + u < J) {
-        x[u] = *reinterpret_cast<const float4*>(slot + (j + u) * step);
-        a[u] = decay[(size_t)(j + u) * p.Hv];
-      }
+  constexpr int kAhead = 8;
+  float4 x[kAhead];
+  float a[kAhead];
+  auto load = [&](int u, int j) {
+    if (j < J) {
+      x[u] = *reinterpret_cast<const float4*>(slot + j * step);
+      a[u] = decay[(size_t)j * p.Hv];
     }
+  };
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < kAhead; ++u) load(u, u);
+  for (int j = 0; j < J; j += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
       if (j + u < J) {
+        const float4 own_x = x[u];
+        const float own_a = a[u];
+        load(u, j + u + kAhead);             // in flight for eight segments' time
         *reinterpret_cast<float4*>(slot + (j + u) * step) = s;
-        s.x = fmaf(a[u], s.x, x[u].x);
-        s.y = fmaf(a[u], s.y, x[u].y);
-        s.z = fmaf(a[u], s.z, x[u].z);
-        s.w = fmaf(a[u], s.w, x[u].w);
+        s.x = fmaf(own_a, s.x, own_x.x);
+        s.y = fmaf(own_a, s.y, own_x.y);
+        s.z = fmaf(own_a, s.z, own_x.z);
+        s.w = fmaf(own_a, s.w, own_x.w);
       }
     }
   }

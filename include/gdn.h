@@ -282,7 +282,7 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  *   g          fp32 log-decay (<= 0 in normal use): [total_T, Hv] with
  *              g_stride = Hv (one for each token and value head), or [Hv] with
  *              g_stride = 0 (one fixed for each value head). -infinity is a
- *              reset: the state before that token counts for nothing from it on.
+ *              reset: a finite state before that token counts for nothing from it on.
  *   state_in   [n_seqs, Hv, dv, dk]  fp32, or NULL for zero states
  *   cu_seqlens [n_seqs + 1] int32, read on the device. Non-decreasing, inside
  *              [0, total_T]; it may begin behind 0 and end before total_T. One
