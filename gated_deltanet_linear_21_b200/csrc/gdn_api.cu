@@ -377,7 +377,9 @@ bool linear_on_tensor_cores(gdn_dtype dtype, int64_t total_T) { return dtype != 
 
 // Blocks of 128 tokens per segment. Fewer make more items, so that one sequence's
 // heads fill the GPU and unequal sequences even out; more make fewer hand-overs of a
-// state. The lengths are on the device: only their mean is known here.
+// state: eight packed sequences of 32 heads take 438 us with up to 8, 456 with up to 4 and
+// 447 with up to 12 (32768 tokens: 469, 487 and 484). The lengths are on the device: only
+// their mean is known here.
 int linear_segment(int n_seqs, int64_t total_T, int Hv) {
   const int64_t per_seq = std::max<int64_t>(1, (total_T / std::max(1, n_seqs) + 127) / 128);
   const int64_t blocks = per_seq * n_seqs * Hv;
