@@ -11,7 +11,7 @@
 // o is computed as rho_r (q_r S + sum_s P'_rs v_s), rho_r = scale exp(G_r), P'_rs =
 // exp(-G_s) q_r . k_s, so that both products go to one accumulator and a score's weight
 // depends on its column alone. That is exact while exp(-G_s) stays in range; a steep block
-// (2^60 or more; f16 2^20) takes a power of two 2^-m_r out of its late rows, from P' by the exponent
+// (2^60 or more) takes a power of two 2^-m_r out of its late rows, from P' by the exponent
 // and from q_r, after Q K^T, exactly.
 //
 // Four products a block, each 128 x 128 x 128: Q K^T, Q S^T, P' V and K~^T V with
@@ -30,8 +30,13 @@
 // 24 bits in bf16. f16 needs hi and rn(w2 k + e1), 22 bits; in bf16 the same two (16
 // bits) serve where the state is only read for o, inside a segment that is not a
 // sequence's last. In f16 powers of two keep what is rounded in the type's range: one
-// from the block's largest |k| and w for the terms of K~, and one from the largest |S| and
-// |P'| for the copy of S and P', which share an accumulator.
+// from the block's largest |k| and w for the terms of K~; 2^-b for the copy of S; and for
+// each row r, whose P' and q meet v and that copy in one accumulator, 2^-a_r for P' and
+// 2^(b - a_r) for q (rho_r holds 2^a_r). No row's or state's size then bears on another's
+// precision: a row's largest score (or q, if that is larger) is at 2^14, or q keeps its size
+// and the score is at 2^3 or above; the largest |S| is at 2^5; what is far below rounds to a
+// multiple of 2^-24. Rows whose scores outweigh their part of the state lose low bits of q so:
+// with |S| at 2^5 that is below 2^-25 of the row's largest score.
 // Log-decays are summed in fp64 (exp(G_r - G_s) of far tokens is a difference of large
 // sums) and clamped where exp is zero in fp32, so that a reset (-inf) does not turn
 // differences into NaN.
@@ -112,11 +117,12 @@ constexpr int kSlices = 32;          // owners of one head's state
 constexpr int kRegsCompute = 176, kRegsOther = 80;
 static_assert(kCompute * kRegsCompute + (kThreads - kCompute) * kRegsOther <= kThreads * 128, "register file");
 constexpr int kStateBytes = kD * kD * 4;
+constexpr float kInf = __builtin_huge_valf();
 constexpr float kMinLog = -105.f;  // exp is 0 in fp32, subnormals included
 
-// A block is steep when its log-decay (base 2) reaches this. In f16 P' has to fit beside the
-// other rows' and the copy of S: 20 bits leave the smallest rows 20 bits below their largest.
-template <typename T> constexpr int kSteep = std::is_same<T, __half>::value ? 20 : 60;
+// A block is steep when its log-decay (base 2) reaches this: P' = exp(-G_s) q_r . k_s and its
+// products with V are fp32 and in bf16 have no other scale, so |q . k| |v| stays below 2^67.
+constexpr int kSteep = 60;
 
 // ---- shared memory (bytes) ----
 constexpr uint32_t kQ = 0;                     // two buffers of [128][128], two K-major 128B-swizzled atoms 16 KB apart;
@@ -670,7 +676,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             gamx[x] = ex2((float)G) * p.scale;
             gbx[x] = ex2((float)-G);
             gpx[x] = (float)(start - G);
-            flat = flat && G > -kSteep<T>;
+            flat = flat && G > -kSteep;
             wm = fmaxf(wm, w[x]);
           }
           uint2 wp[3];
@@ -851,7 +857,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     uint8_t* slots = p.ws + Workspace::slots_offset(G) + (size_t)cta * 4 * kStateBytes;
     uint32_t cnt = 0, qn = 0, rn = 0, phases = 0;   // phases: the parity that each barrier is waited for next
     float S[64];        // S[64 wg + i][row]
-    float up = 1.f;     // f16: P' and the copy of S are divided by it
+    float up = 1.f;     // f16: 2^a of this thread's row
     float seg_gam = 1.f;
 
     auto wait_next = [&](int bar) {
@@ -912,8 +918,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           for (int i = 0; i < 16; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&kr[i])));
         }
         const float2 f = __half22float2(m);
-        // |w k| below 2^14 and w below 2^15
-        e = min(13 - exponent_of(reduce_max(fmaxf(f.x, f.y)) * misc->w_max), 14 - exponent_of(misc->w_max));
+        // |w k| below 2^14 and w below 2^15 (an infinite k leaves the others their size)
+        e = min(13 - exponent_of(fminf(reduce_max(fmaxf(f.x, f.y)), 65504.f) * misc->w_max), 14 - exponent_of(misc->w_max));
         const float scale = pow2i(e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -992,18 +998,61 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       tc_fence_before();
       arrive_warp(&bars[kURead + q]);
     };
-    // f16: the power of two that P' and the copy of S share, from the larger of the two (so S
-    // has to be there): sets `up`, returns its inverse.
-    auto common_scale = [&](float top) {
+    // f16: the powers of two of the copy of S (2^-b, returned) and of this thread's row (P' by
+    // `by` = 2^-a, q by 2^(b - a - m), `up` = 2^a), from the largest |S|, |P'| (`top`: of the
+    // thread's 64 columns) and |q|; S has to be there. `rows`, 512 bytes of the tables that this
+    // block has no use for, holds each half row's exponents of |P'| and |q|. (They are written
+    // after Q K^T of this block, which follows every warp's copy of S in the block before.)
+    auto row_scales = [&](float top, uint8_t* q, int m, float* rows, float& by) -> float {
+      uint4* const qr = reinterpret_cast<uint4*>(q + wg * 16384 + row * 128);
+      __half2 mq = __half2half2(__ushort_as_half(0));
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {
+        const uint4 x = qr[c ^ (row & 7)];
+        mq = __hmax2(__hmax2(__hmax2(mq, __habs2(*reinterpret_cast<const __half2*>(&x.x))),
+                             __hmax2(__habs2(*reinterpret_cast<const __half2*>(&x.y)),
+                                     __habs2(*reinterpret_cast<const __half2*>(&x.z)))),
+                     __habs2(*reinterpret_cast<const __half2*>(&x.w)));
+      }
+      const float2 f = __half22float2(mq);
+      uint16_t* const er = reinterpret_cast<uint16_t*>(rows) + row;
+      er[128 * wg] = (uint16_t)((exponent_of(top) + 127) << 8 | (exponent_of(fmaxf(f.x, f.y)) + 127));
+      float most;
+      bool finite = true;
+#pragma unroll 1
+      do {   // again where there are infinities: the other values keep their size
+        most = 0.f;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) top = fmaxf(top, fabsf(S[i]));
-      const int e = exponent_of(reduce_max(top)) - 14;   // the largest below 2^15
-      up = pow2i(e);
-      return pow2i(-e);
+        for (int i = 0; i < 64; ++i) most = finite || fabsf(S[i]) < kInf ? fmaxf(most, fabsf(S[i])) : most;
+        most = reduce_max(most);
+        finite = !finite || most < kInf;
+      } while (!finite);
+      const uint32_t x = er[0], y = er[128];
+      const int b = max(exponent_of(most) - 5, -100);
+      const int ep = (int)max(x >> 8, y >> 8) - 127, eq = (int)max(x & 255u, y & 255u) - 127 - m;
+      // q as it is where the scores have their place beside it
+      const int a = m == 0 && ep >= b + 3 && ep <= b + 14 ? b : max(max(ep, b + eq) - 14, max(b - m - 30, -100));
+      up = pow2i(a);
+      by = pow2i(-a);
+      const int c = b - a - m;
+      if (__any_sync(0xffffffffu, c != 0)) {
+        // (two factors: f16 holds no power below 2^-24)
+        const __half2 f1 = __float2half2_rn(pow2i(min(max(c, -14), 15)));
+        const __half2 f2 = __float2half2_rn(pow2i(min(max(c + 14, -25), 0) + max(c - 15, 0)));
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          uint4 z = qr[i ^ (row & 7)];
+          __half2* const h = reinterpret_cast<__half2*>(&z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = __hmul2(__hmul2(h[j], f1), f2);
+          qr[i ^ (row & 7)] = z;
+        }
+      }
+      return pow2i(-b);
     };
     // P', packed, over Q K^T: 32 rows and 64 columns, zero above the diagonal.
-    auto make_scores = [&](int L) {
-      float down = 1.f, top = 0.f;
+    auto make_scores = [&](uint8_t* q) {
+      float down = 1.f, by = 1.f, top = 0.f;
 #pragma unroll 1
       for (int pass = kF16 ? 0 : 1; pass < 2; ++pass) {
 #pragma unroll 1
@@ -1031,7 +1080,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
                 for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
               }
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] *= down;
+              for (int i = 0; i < 32; ++i) x[i] *= by;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) u[i] = Op16<T>::pack2(x[2 * i], x[2 * i + 1]);
@@ -1039,7 +1088,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           if (pass == 1) tmem_st16(tl + kColP + 16 * c, u);   // (columns that this warp has read)
         }
         if constexpr (kF16) {
-          if (pass == 0) down = common_scale(row < L ? top : 0.f);
+          if (pass == 0) down = row_scales(top, q, 0, tab_gp, by);
         }
       }
       tmem_wait_st();
@@ -1047,18 +1096,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       return down;
     };
     // A steep block's: 2^-m_r out of a row of Q, and P' by the exponent; compact, not fast.
-    auto make_steep_scores = [&](int L, uint8_t* q, int m_row) {
-      const float f = m_row > 126 ? 0.f : pow2i(-m_row);
+    auto make_steep_scores = [&](uint8_t* q, int m_row) {
+      if constexpr (!kF16) {
+        const float f = m_row > 126 ? 0.f : pow2i(-m_row);
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint4* at = reinterpret_cast<uint4*>(q + wg * 16384 + row * 128 + ((c ^ (row & 7)) << 4));
-        float x[8];
-        unpack8<T>(*at, x);
+        for (int c = 0; c < 8; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(q + wg * 16384 + row * 128 + ((c ^ (row & 7)) << 4));
+          float x[8];
+          unpack8<T>(*at, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f;
-        *at = pack8<T>(x);
+          for (int i = 0; i < 8; ++i) x[i] *= f;
+          *at = pack8<T>(x);
+        }
       }
-      float down = 1.f, top = 0.f;
+      float down = 1.f, by = 1.f, top = 0.f;
 #pragma unroll 1
       for (int pass = kF16 ? 0 : 1; pass < 2; ++pass) {
 #pragma unroll 1
@@ -1075,11 +1126,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           if (pass == 1) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tmem_st1(tl + kColP + 4 * c + i, Op16<T>::pack2(x[2 * i] * down, x[2 * i + 1] * down));
+              tmem_st1(tl + kColP + 4 * c + i, Op16<T>::pack2(x[2 * i] * by, x[2 * i + 1] * by));
           }
         }
         if constexpr (kF16) {
-          if (pass == 0) down = common_scale(row < L ? top : 0.f);
+          if (pass == 0) down = row_scales(top, q, m_row, tab_gb, by);
         }
       }
       tmem_wait_st();
@@ -1200,11 +1251,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
               rho = tab_gam[row];
               if (steep) {
                 const float rest = misc->start_f[w4] - tab_gp[row];
-                const int m_row = max(0, -kSteep<T> - misc->start_i[w4] - (int)ceilf(rest));
+                const int m_row = max(0, -kSteep - misc->start_i[w4] - (int)ceilf(rest));
                 rho = p.scale * ex2((float)(misc->start_i[w4] + m_row) + rest);
-                down = make_steep_scores(L, q_tile, m_row);
+                down = make_steep_scores(q_tile, m_row);
               } else {
-                down = make_scores(L);
+                down = make_scores(q_tile);
               }
             }
             if (here && !four) arrive_warp(&bars[kTabEmpty]);

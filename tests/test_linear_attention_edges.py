@@ -1,0 +1,56 @@
+"""Decayed linear attention at values and calls where it could go wrong: tokens of
+unlike size in one block, and what follows below. References and bounds are those
+of tests/_linear_ref.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests import _linear_ref as ref
+from tests.test_linear_attention import check, draw, prefill
+
+gdn = pytest.importorskip("gated_deltanet_linear_21_b200")
+
+DEV = "cuda"
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+# ------------------------------------------ tokens of unlike size in a block ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("at", [0, 63, 100, 127, 200])
+@pytest.mark.parametrize("grow,v", [(128, 0), (512, -8), (4096, -14)], ids=str)
+def test_a_large_token_leaves_the_others_of_its_block_as_they_were(dtype, at, grow, v):
+    """One token's q and k enlarged (its v small, so that every output stays in f16's
+    range), in a block that decays by 18 bits: the other rows keep their precision."""
+    x = draw([256], 1, 2, 128, 128, dtype, seed=70)
+    x["g"] = torch.full((2,), -18 * 0.6931 / 128)
+    for n in ("q", "k"):
+        x[n][at] = (x[n][at].float() * grow).to(dtype)
+    x["v"][at] = (x["v"][at].float() * 2.0 ** v).to(dtype)
+    check(x, *prefill(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bits", [1, 18, 45, 100])
+def test_rows_of_every_size_in_a_block(dtype, bits):
+    """q and k of each token, and the state, at their own powers of two."""
+    x = draw([300, 130], 2, 2, 128, 64, dtype, seed=71)
+    gen = torch.Generator().manual_seed(72)
+    size = lambda lo, hi, n: torch.exp2(torch.randint(lo, hi + 1, (n, 1, 1), generator=gen).float())  # noqa: E731
+    x["q"] = (x["q"].float() * size(-12, 4, 430)).to(dtype)
+    x["k"] = (x["k"].float() * size(-6, 4, 430)).to(dtype)
+    x["state_in"][0] *= 2.0 ** 12
+    x["state_in"][1] *= 2.0 ** -12
+    x["g"] = torch.full((2,), -bits * 0.6931 / 128)
+    o, s = prefill(x)
+    ro, rs, mo, ms = ref.linear_prefill(x["q"], x["k"], x["v"], x["g"], x["state_in"], x["cu"])
+    # rounding to nearest makes what is 65520 or more infinite in f16; the error before it is within 2^-10 mo
+    near = np.abs(ro) + 2.0 ** -10 * mo >= 65520 if dtype == F16 else np.zeros(ro.shape, bool)
+    got = ref.f64(o)
+    assert (np.isfinite(got) | (near & (np.sign(got) == np.sign(ro)))).all()
+    o = torch.where(torch.from_numpy(near & ~np.isfinite(got)).to(DEV), 0, o)
+    ref.check_o(o, np.where(near & ~np.isfinite(got), 0, ro), mo, 300, 128)
+    ref.check_state(s, rs, ms, 300)
