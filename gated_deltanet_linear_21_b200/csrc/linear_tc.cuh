@@ -115,6 +115,7 @@ constexpr int kSlices = 32;          // owners of one head's state
 // Registers: 512 threads start with 128 each; the compute warps' share grows by what the
 // others give back (256 x 176 + 256 x 80 = 65536, all that the block holds).
 constexpr int kRegsCompute = 176, kRegsOther = 80;
+static_assert(kLoadWarp == kComputeWarps && kComputeWarps % 4 == 0 && kWarps % 4 == 0, "whole groups of four warps");
 static_assert(kCompute * kRegsCompute + (kThreads - kCompute) * kRegsOther <= kThreads * 128, "register file");
 constexpr int kStateBytes = kD * kD * 4;
 constexpr float kInf = __builtin_huge_valf();
@@ -584,269 +585,268 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   };
   Item it;
 
-  if (warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
+    // (one instruction for the four warps of a group, as it has to be: before the roles part)
     give_registers();
-    // ------------------------------------------------- items; K, V tiles ---
-    const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
-    Walk walk;
-    uint32_t cnt = 0;
-    bool more = true;
-    for (uint32_t i = 0; more && wait.ok(); ++i) {
-      more = walk.find(p, cta + (int)i * G, it);
-      if (!more) it.n = -1;
-      if (i >= kRingItems) wait(&bars[kItEmpty + (i & 3)], ((i >> 2) - 1) & 1);
-      if (lane == 0) ring[i & 3] = it;
-      arrive_warp(&bars[kItFull + (i & 3)]);
-      if (!more) break;
-      const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
-      const bool shared_k = p.Hv != p.Hqk;
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------- items; K, V tiles ---
+      const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+      Walk walk;
+      uint32_t cnt = 0;
+      bool more = true;
+      for (uint32_t i = 0; more && wait.ok(); ++i) {
+        more = walk.find(p, cta + (int)i * G, it);
+        if (!more) it.n = -1;
+        if (i >= kRingItems) wait(&bars[kItEmpty + (i & 3)], ((i >> 2) - 1) & 1);
+        if (lane == 0) ring[i & 3] = it;
+        arrive_warp(&bars[kItFull + (i & 3)]);
+        if (!more) break;
+        const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
+        const bool shared_k = p.Hv != p.Hqk;
 #pragma unroll 1
-      for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
+        for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
 #pragma unroll 1
-        for (int b = 0; b < nb; ++b, ++cnt) {
-          const uint32_t s = cnt & 1;
-          if (cnt >= 2) wait(&bars[kKvEmpty + s], ((cnt >> 1) - 1) & 1);
-          if (!wait.ok()) break;
-          const int t = it.t0 + b * kB;
-          uint64_t* full = &bars[kKvFull + s];
-          mbar_arrive_expect_tx_warp(full, 65536);
-          uint8_t *kt = sm + kK + s * 32768, *vt = sm + kV + s * 32768;
-          // the second pass is the last to read V, and K where no other head shares it
-          const uint64_t pv = pass == 0 ? again : once, pk = pass == 0 || shared_k ? again : once;
-          tma_load_3d_warp_hint(kt, &km, full, 0, hq, t, pk);
-          tma_load_3d_warp_hint(kt + 16384, &km, full, 64, hq, t, pk);
-          tma_load_3d_warp_hint(vt, &vm, full, 0, it.h, t, pv);
-          tma_load_3d_warp_hint(vt + 16384, &vm, full, 64, it.h, t, pv);
+          for (int b = 0; b < nb; ++b, ++cnt) {
+            const uint32_t s = cnt & 1;
+            if (cnt >= 2) wait(&bars[kKvEmpty + s], ((cnt >> 1) - 1) & 1);
+            if (!wait.ok()) break;
+            const int t = it.t0 + b * kB;
+            uint64_t* full = &bars[kKvFull + s];
+            mbar_arrive_expect_tx_warp(full, 65536);
+            uint8_t *kt = sm + kK + s * 32768, *vt = sm + kV + s * 32768;
+            // the second pass is the last to read V, and K where no other head shares it
+            const uint64_t pv = pass == 0 ? again : once, pk = pass == 0 || shared_k ? again : once;
+            tma_load_3d_warp_hint(kt, &km, full, 0, hq, t, pk);
+            tma_load_3d_warp_hint(kt + 16384, &km, full, 64, hq, t, pk);
+            tma_load_3d_warp_hint(vt, &vm, full, 0, it.h, t, pv);
+            tma_load_3d_warp_hint(vt + 16384, &vm, full, 64, it.h, t, pv);
+          }
         }
       }
-    }
-    // tiles still on their way land before the CTA ends
-    for (uint32_t c = cnt >= 2 ? cnt - 2 : 0; c < cnt; ++c) mbar_wait(&bars[kKvFull + (c & 1)], (c >> 1) & 1);
-  } else if (warp == kGateWarp) {
-    give_registers();
-    // ------------------------------------------- Q tiles and decay tables ---
-    const uint64_t pol = p.Hv != p.Hqk ? l2_evict_normal_policy() : l2_evict_first_policy();
-    uint32_t qn = 0, cnt = 0;
+      // tiles still on their way land before the CTA ends
+      for (uint32_t c = cnt >= 2 ? cnt - 2 : 0; c < cnt; ++c) mbar_wait(&bars[kKvFull + (c & 1)], (c >> 1) & 1);
+    } else if (warp == kGateWarp) {
+      // ------------------------------------------- Q tiles and decay tables ---
+      const uint64_t pol = p.Hv != p.Hqk ? l2_evict_normal_policy() : l2_evict_first_policy();
+      uint32_t qn = 0, cnt = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; next_item(i, it); ++i) {
-      const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
-      const float* gh = p.g + it.h;
+      for (uint32_t i = 0; next_item(i, it); ++i) {
+        const int hq = it.h / (p.Hv / p.Hqk), nb = (it.len + kB - 1) / kB;
+        const float* gh = p.g + it.h;
 #pragma unroll 1
-      for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
-        double seg = 0.0;
-        float g[4];
-        // a block's log-decays, four consecutive tokens to a lane, fetched a block ahead
-        auto fetch = [&](int b) {
-          const int r = b * kB + 4 * lane;
+        for (int pass = it.j + 1 < it.J ? 0 : 1; pass < 2; ++pass) {
+          double seg = 0.0;
+          float g[4];
+          // a block's log-decays, four consecutive tokens to a lane, fetched a block ahead
+          auto fetch = [&](int b) {
+            const int r = b * kB + 4 * lane;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            g[x] = r + x < it.len ? gh[(size_t)(it.t0 + r + x) * p.g_stride] : 0.f;
-        };
-        fetch(0);
+            for (int x = 0; x < 4; ++x)
+              g[x] = r + x < it.len ? gh[(size_t)(it.t0 + r + x) * p.g_stride] : 0.f;
+          };
+          fetch(0);
 #pragma unroll 1
-        for (int b = 0; b < nb && wait.ok(); ++b, ++cnt) {
-          const int L = min(kB, it.len - b * kB);
-          // G, the log-decays (base 2) from the block's start, in fp64; rounded to fp32 as
-          // differences only
-          constexpr double kLog2E = 1.4426950408889634;
-          double c[4];
+          for (int b = 0; b < nb && wait.ok(); ++b, ++cnt) {
+            const int L = min(kB, it.len - b * kB);
+            // G, the log-decays (base 2) from the block's start, in fp64; rounded to fp32 as
+            // differences only
+            constexpr double kLog2E = 1.4426950408889634;
+            double c[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            c[x] = (g[x] < kMinLog ? kMinLog : g[x]) * kLog2E;
-            if (x > 0) c[x] += c[x - 1];
-          }
-          double incl = c[3];
-          fetch(b + 1);
+            for (int x = 0; x < 4; ++x) {
+              c[x] = (g[x] < kMinLog ? kMinLog : g[x]) * kLog2E;
+              if (x > 0) c[x] += c[x - 1];
+            }
+            double incl = c[3];
+            fetch(b + 1);
 #pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-          }
-          const double sum = __shfl_sync(0xffffffffu, incl, 31), before = incl - c[3];
-          const double start = __shfl_sync(0xffffffffu, before, lane & 24), whole = floor(start);
-          seg += sum;
-          float w[4], wm = 0.f;
-          float4 gam, gb, gp;
-          float *const gamx = &gam.x, *const gbx = &gb.x, *const gpx = &gp.x;
-          bool flat = true;
+            for (int off = 1; off < 32; off <<= 1) {
+              const double y = __shfl_up_sync(0xffffffffu, incl, off);
+              if (lane >= off) incl += y;
+            }
+            const double sum = __shfl_sync(0xffffffffu, incl, 31), before = incl - c[3];
+            const double start = __shfl_sync(0xffffffffu, before, lane & 24), whole = floor(start);
+            seg += sum;
+            float w[4], wm = 0.f;
+            float4 gam, gb, gp;
+            float *const gamx = &gam.x, *const gbx = &gb.x, *const gpx = &gp.x;
+            bool flat = true;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const double G = before + c[x];
-            w[x] = 4 * lane + x < L ? ex2((float)(sum - G)) : 0.f;
-            gamx[x] = ex2((float)G) * p.scale;
-            gbx[x] = ex2((float)-G);
-            gpx[x] = (float)(start - G);
-            flat = flat && G > -kSteep;
-            wm = fmaxf(wm, w[x]);
-          }
-          uint2 wp[3];
-          if constexpr (kF16) {
+            for (int x = 0; x < 4; ++x) {
+              const double G = before + c[x];
+              w[x] = 4 * lane + x < L ? ex2((float)(sum - G)) : 0.f;
+              gamx[x] = ex2((float)G) * p.scale;
+              gbx[x] = ex2((float)-G);
+              gpx[x] = (float)(start - G);
+              flat = flat && G > -kSteep;
+              wm = fmaxf(wm, w[x]);
+            }
+            uint2 wp[3];
+            if constexpr (kF16) {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
-          } else {
-            float v[4] = {w[0], w[1], w[2], w[3]};
+              for (int off = 16; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
+            } else {
+              float v[4] = {w[0], w[1], w[2], w[3]};
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              wp[term] = make_uint2(Op16<T>::pack2(v[0], v[1]), Op16<T>::pack2(v[2], v[3]));
-              const float2 lo = Op16<T>::unpack2(wp[term].x), hi = Op16<T>::unpack2(wp[term].y);
-              v[0] -= lo.x; v[1] -= lo.y; v[2] -= hi.x; v[3] -= hi.y;
+              for (int term = 0; term < 3; ++term) {
+                wp[term] = make_uint2(Op16<T>::pack2(v[0], v[1]), Op16<T>::pack2(v[2], v[3]));
+                const float2 lo = Op16<T>::unpack2(wp[term].x), hi = Op16<T>::unpack2(wp[term].y);
+                v[0] -= lo.x; v[1] -= lo.y; v[2] -= hi.x; v[3] -= hi.y;
+              }
+            }
+            const uint32_t steep = __any_sync(0xffffffffu, !flat);
+            const float gam_l = ex2((float)sum), seg_gam = ex2((float)seg), rest = (float)(start - whole);
+            const int whole_i = (int)whole;
+            // everything is ready before the tables may be written: they are one block's
+            if (cnt > 0) wait(&bars[kTabEmpty], (cnt - 1) & 1);
+            if constexpr (kF16) {
+              reinterpret_cast<float4*>(tab_w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+              for (int term = 0; term < 3; ++term) reinterpret_cast<uint2*>(tab_wp + 64 * term)[lane] = wp[term];
+            }
+            reinterpret_cast<float4*>(tab_gam)[lane] = gam;
+            reinterpret_cast<float4*>(tab_gp)[lane] = gp;
+            reinterpret_cast<float4*>(tab_gb)[lane] = gb;
+            if ((lane & 7) == 0) {
+              misc->start_i[lane >> 3] = whole_i;
+              misc->start_f[lane >> 3] = rest;
+            }
+            if (lane == 0) {
+              misc->w_max = wm;
+              misc->steep = steep;
+              misc->gam_l = gam_l;
+              misc->seg_gam = seg_gam;
+            }
+            arrive_warp(&bars[kKvFull + (cnt & 1)]);   // (the block is there when K, V and these are)
+            if (pass == 1) {
+              const uint32_t q = qn & 1;
+              if (qn >= 2) wait(&bars[kQFree + q], ((qn >> 1) - 1) & 1);
+              if (wait.ok()) {
+                mbar_arrive_expect_tx_warp(&bars[kQFull + q], 32768);
+                tma_load_3d_warp_hint(sm + kQ + q * 32768, &qm, &bars[kQFull + q], 0, hq, it.t0 + b * kB, pol);
+                tma_load_3d_warp_hint(sm + kQ + q * 32768 + 16384, &qm, &bars[kQFull + q], 64, hq, it.t0 + b * kB, pol);
+                ++qn;
+              }
             }
           }
-          const uint32_t steep = __any_sync(0xffffffffu, !flat);
-          const float gam_l = ex2((float)sum), seg_gam = ex2((float)seg), rest = (float)(start - whole);
-          const int whole_i = (int)whole;
-          // everything is ready before the tables may be written: they are one block's
-          if (cnt > 0) wait(&bars[kTabEmpty], (cnt - 1) & 1);
-          if constexpr (kF16) {
-            reinterpret_cast<float4*>(tab_w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
-          } else {
-#pragma unroll
-            for (int term = 0; term < 3; ++term) reinterpret_cast<uint2*>(tab_wp + 64 * term)[lane] = wp[term];
-          }
-          reinterpret_cast<float4*>(tab_gam)[lane] = gam;
-          reinterpret_cast<float4*>(tab_gp)[lane] = gp;
-          reinterpret_cast<float4*>(tab_gb)[lane] = gb;
-          if ((lane & 7) == 0) {
-            misc->start_i[lane >> 3] = whole_i;
-            misc->start_f[lane >> 3] = rest;
-          }
-          if (lane == 0) {
-            misc->w_max = wm;
-            misc->steep = steep;
-            misc->gam_l = gam_l;
-            misc->seg_gam = seg_gam;
-          }
-          arrive_warp(&bars[kKvFull + (cnt & 1)]);   // (the block is there when K, V and these are)
-          if (pass == 1) {
-            const uint32_t q = qn & 1;
-            if (qn >= 2) wait(&bars[kQFree + q], ((qn >> 1) - 1) & 1);
-            if (wait.ok()) {
-              mbar_arrive_expect_tx_warp(&bars[kQFull + q], 32768);
-              tma_load_3d_warp_hint(sm + kQ + q * 32768, &qm, &bars[kQFull + q], 0, hq, it.t0 + b * kB, pol);
-              tma_load_3d_warp_hint(sm + kQ + q * 32768 + 16384, &qm, &bars[kQFull + q], 64, hq, it.t0 + b * kB, pol);
+        }
+      }
+      for (uint32_t q = qn >= 2 ? qn - 2 : 0; q < qn; ++q) mbar_wait(&bars[kQFull + (q & 1)], (q >> 1) & 1);
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------- tensor-core work ---
+      constexpr uint32_t id_qk = idesc_f16kind(128, 128, false, false, kFmt);   // both K-major
+      constexpr uint32_t id_mn = idesc_f16kind(128, 128, false, true, kFmt);    // B MN-major
+      // (one copy of each product's code: the loops of all roles share the instruction cache)
+      uint32_t cnt = 0, qn = 0, tn0 = 0, tn1 = 0, un0 = 0, un1 = 0;   // tn, un: uses of kKt and the accumulators
+#pragma unroll 1
+      for (uint32_t i = 0; next_item(i, it); ++i) {
+        const int nb = (it.len + kB - 1) / kB;
+        const bool last = it.j + 1 == it.J;
+#pragma unroll 1
+        for (int pass = last ? 1 : 0; pass < 2; ++pass) {
+          const bool a = pass == 0;
+#pragma unroll 1
+          for (int b = 0; b < nb && wait.ok(); ++b, ++cnt) {
+            const bool a = each_time(pass == 0);
+            const uint32_t s = cnt & 1;
+            const uint64_t vd = desc_mnmajor(sbase + kV + s * 32768, 0, 128, 16384);
+            const uint64_t qd = desc_kmajor(sbase + kQ + (qn & 1) * 32768, 0, 16384);
+            wait(&bars[kKvFull + s], (cnt >> 1) & 1);
+            if (!a) {
+              wait(&bars[kQFull + (qn & 1)], (qn >> 1) & 1);
+              tc_fence_after();
+              const uint64_t kd = desc_kmajor(sbase + kK + s * 32768, 0, 16384);
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h)
+                mma_run_warp<4, 2, 2>(tmem + kColP, desc_advance(qd, 16384 * h), desc_advance(kd, 16384 * h), id_qk, h);
+              mma_commit_warp(&bars[kPFull]);
+            }
+            if (a || last || b + 1 < nb) {   // (the state after another segment comes from pass A)
+              const uint32_t q = a ? b & 1 : 0, used = q ? un1++ : un0++;
+              if (a && b >= 2) wait(&bars[kURead + q], (used - 1) & 1);
+              // Two terms of K~ at a time. Pass A has room for two such pairs, so one is made while
+              // the other is multiplied: the block's other two (bf16), or the next block's (f16).
+              const int parts = !kF16 && (a || last) ? 2 : 1;
+#pragma unroll 1
+              for (int part = 0; part < parts; ++part) {
+                const uint32_t r = parts == 2 ? part : a ? b & 1 : 0;
+                wait(&bars[kKt + r], (r ? tn1++ : tn0++) & 1);
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x)   // the smaller term first, either half of the tokens
+                  mma4_tmem_a_run_warp<128>(tmem + (q ? kColP : kColU),
+                                            tmem + (a && r ? kColO : kColK) + (x < 2 ? 32 : 0) + 64 * (x & 1),
+                                            desc_advance(vd, 8192 * (x & 1)), id_mn, part | x);
+                if (a || part + 1 < parts) mma_commit_warp(&bars[kHalf + r]);
+              }
+              mma_commit_warp(&bars[kUFull + q]);
+            }
+            if (!a) {
+              wait(&bars[kSReady], qn & 1);
+              tc_fence_after();
+              const uint64_t sd = desc_mnmajor(sbase + kS, 0, 128, 16384);
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h)
+                mma_run_warp<4, 2, 128>(tmem + kColO, desc_advance(qd, 16384 * h), desc_advance(sd, 8192 * h), id_mn, h);
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h)
+                mma4_tmem_a_run_warp<128>(tmem + kColO, tmem + kColP + 64 * h, desc_advance(vd, 8192 * h), id_mn, 1);
+              mma_commit_warp(&bars[kOFull]);
               ++qn;
             }
+            mma_commit_warp(&bars[kKvEmpty + s]);
+          }
+          if (a) {   // both accumulators are read before pass B reuses their columns
+            wait(&bars[kURead], (un0 - 1) & 1);
+            if (nb > 1) wait(&bars[kURead + 1], (un1 - 1) & 1);
           }
         }
       }
-    }
-    for (uint32_t q = qn >= 2 ? qn - 2 : 0; q < qn; ++q) mbar_wait(&bars[kQFull + (q & 1)], (q >> 1) & 1);
-  } else if (warp == kMmaWarp) {
-    give_registers();
-    // ------------------------------------------------- tensor-core work ---
-    constexpr uint32_t id_qk = idesc_f16kind(128, 128, false, false, kFmt);   // both K-major
-    constexpr uint32_t id_mn = idesc_f16kind(128, 128, false, true, kFmt);    // B MN-major
-    // (one copy of each product's code: the loops of all roles share the instruction cache)
-    uint32_t cnt = 0, qn = 0, tn0 = 0, tn1 = 0, un0 = 0, un1 = 0;   // tn, un: uses of kKt and the accumulators
+    } else if (warp == kCourierWarp) {
+      // ---------------------------------------------- flags in global memory ---
+      if (p.ws) {
+        uint32_t* all = reinterpret_cast<uint32_t*>(p.ws);
+        uint32_t* flags = all + cta * kFlagWords;
+        uint32_t pubs0 = 0, pubs1 = 0, ins0 = 0, ins1 = 0, pn = 0;   // uses of this CTA's slots, by parity
 #pragma unroll 1
-    for (uint32_t i = 0; next_item(i, it); ++i) {
-      const int nb = (it.len + kB - 1) / kB;
-      const bool last = it.j + 1 == it.J;
-#pragma unroll 1
-      for (int pass = last ? 1 : 0; pass < 2; ++pass) {
-        const bool a = pass == 0;
-#pragma unroll 1
-        for (int b = 0; b < nb && wait.ok(); ++b, ++cnt) {
-          const bool a = each_time(pass == 0);
-          const uint32_t s = cnt & 1;
-          const uint64_t vd = desc_mnmajor(sbase + kV + s * 32768, 0, 128, 16384);
-          const uint64_t qd = desc_kmajor(sbase + kQ + (qn & 1) * 32768, 0, 16384);
-          wait(&bars[kKvFull + s], (cnt >> 1) & 1);
-          if (!a) {
-            wait(&bars[kQFull + (qn & 1)], (qn >> 1) & 1);
-            tc_fence_after();
-            const uint64_t kd = desc_kmajor(sbase + kK + s * 32768, 0, 16384);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h)
-              mma_run_warp<4, 2, 2>(tmem + kColP, desc_advance(qd, 16384 * h), desc_advance(kd, 16384 * h), id_qk, h);
-            mma_commit_warp(&bars[kPFull]);
-          }
-          if (a || last || b + 1 < nb) {   // (the state after another segment comes from pass A)
-            const uint32_t q = a ? b & 1 : 0, used = q ? un1++ : un0++;
-            if (a && b >= 2) wait(&bars[kURead + q], (used - 1) & 1);
-            // Two terms of K~ at a time. Pass A has room for two such pairs, so one is made while
-            // the other is multiplied: the block's other two (bf16), or the next block's (f16).
-            const int parts = !kF16 && (a || last) ? 2 : 1;
-#pragma unroll 1
-            for (int part = 0; part < parts; ++part) {
-              const uint32_t r = parts == 2 ? part : a ? b & 1 : 0;
-              wait(&bars[kKt + r], (r ? tn1++ : tn0++) & 1);
-              tc_fence_after();
-#pragma unroll 1
-              for (int x = 0; x < 4; ++x)   // the smaller term first, either half of the tokens
-                mma4_tmem_a_run_warp<128>(tmem + (q ? kColP : kColU),
-                                          tmem + (a && r ? kColO : kColK) + (x < 2 ? 32 : 0) + 64 * (x & 1),
-                                          desc_advance(vd, 8192 * (x & 1)), id_mn, part | x);
-              if (a || part + 1 < parts) mma_commit_warp(&bars[kHalf + r]);
+        for (uint32_t i = 0; next_item(i, it); ++i) {
+          const int par = i & 1;
+          const bool last = it.j + 1 == it.J;
+          if (!last) {
+            const uint32_t used = par ? pubs1++ : pubs0++;
+            if (lane == 0 && used > 0) wait.flag(flags + kScanned + par, kSlices * used);
+            arrive_warp(&bars[kSlotFree]);
+            wait(&bars[kPub], pn++ & 1);
+            if (lane == 0) {
+              fence_acq_rel_gpu();
+              st_relaxed_gpu(flags + kOutReady + par, i + 1);
             }
-            mma_commit_warp(&bars[kUFull + q]);
           }
-          if (!a) {
-            wait(&bars[kSReady], qn & 1);
-            tc_fence_after();
-            const uint64_t sd = desc_mnmajor(sbase + kS, 0, 128, 16384);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h)
-              mma_run_warp<4, 2, 128>(tmem + kColO, desc_advance(qd, 16384 * h), desc_advance(sd, 8192 * h), id_mn, h);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h)
-              mma4_tmem_a_run_warp<128>(tmem + kColO, tmem + kColP + 64 * h, desc_advance(vd, 8192 * h), id_mn, 1);
-            mma_commit_warp(&bars[kOFull]);
-            ++qn;
+          if (it.j > 0) {
+            const uint32_t use = par ? ++ins1 : ++ins0;
+            if (lane == 0) wait.flag(flags + kInCnt + par, kSlices * use);
+            arrive_warp(&bars[kInReady]);
           }
-          mma_commit_warp(&bars[kKvEmpty + s]);
-        }
-        if (a) {   // both accumulators are read before pass B reuses their columns
-          wait(&bars[kURead], (un0 - 1) & 1);
-          if (nb > 1) wait(&bars[kURead + 1], (un1 - 1) & 1);
-        }
-      }
-    }
-  } else if (warp == kCourierWarp) {
-    give_registers();
-    // ---------------------------------------------- flags in global memory ---
-    if (p.ws) {
-      uint32_t* all = reinterpret_cast<uint32_t*>(p.ws);
-      uint32_t* flags = all + cta * kFlagWords;
-      uint32_t pubs0 = 0, pubs1 = 0, ins0 = 0, ins1 = 0, pn = 0;   // uses of this CTA's slots, by parity
-  #pragma unroll 1
-    for (uint32_t i = 0; next_item(i, it); ++i) {
-        const int par = i & 1;
-        const bool last = it.j + 1 == it.J;
-        if (!last) {
-          const uint32_t used = par ? pubs1++ : pubs0++;
-          if (lane == 0 && used > 0) wait.flag(flags + kScanned + par, kSlices * used);
-          arrive_warp(&bars[kSlotFree]);
-          wait(&bars[kPub], pn++ & 1);
+          wait(&bars[kGot + (i & 3)], (i >> 2) & 1);
           if (lane == 0) {
             fence_acq_rel_gpu();
-            st_relaxed_gpu(flags + kOutReady + par, i + 1);
+            st_relaxed_gpu(flags + kDone, i + 1);
           }
+          if (last && it.J > 1) {
+            // state_out may be state_in, whose reader is then the first segment
+            if (lane == 0) wait.flag(all + (it.first % G) * kFlagWords + kDone, it.first / G + 1);
+            arrive_warp(&bars[kOutOk]);
+          }
+          arrive_warp(&bars[kItEmpty + (i & 3)]);
         }
-        if (it.j > 0) {
-          const uint32_t use = par ? ++ins1 : ++ins0;
-          if (lane == 0) wait.flag(flags + kInCnt + par, kSlices * use);
-          arrive_warp(&bars[kInReady]);
-        }
-        wait(&bars[kGot + (i & 3)], (i >> 2) & 1);
-        if (lane == 0) {
-          fence_acq_rel_gpu();
-          st_relaxed_gpu(flags + kDone, i + 1);
-        }
-        if (last && it.J > 1) {
-          // state_out may be state_in, whose reader is then the first segment
-          if (lane == 0) wait.flag(all + (it.first % G) * kFlagWords + kDone, it.first / G + 1);
-          arrive_warp(&bars[kOutOk]);
-        }
-        arrive_warp(&bars[kItEmpty + (i & 3)]);
       }
+    } else if (warp >= kScanWarp) {
+      // ------------------------------------- states between the segments ---
+      if (p.ws) scan_role(p, cta * kScanWarps + warp - kScanWarp, G);
     }
-  } else if (warp >= kScanWarp) {
-    give_registers();
-    // ------------------------------------- states between the segments ---
-    if (p.ws) scan_role(p, cta * kScanWarps + warp - kScanWarp, G);
   } else {
-    take_registers();
+    take_registers();   // waits until the others have given theirs
     // ----------------------------------------------------- compute warps ---
     // Warp w4 of each four has lanes 32 w4 .. of tensor memory: rows (tokens) of P and o,
     // columns (d_k) of K~ and of the state. wg: the half of the tokens of K~, of the

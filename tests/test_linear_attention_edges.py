@@ -2,6 +2,9 @@
 unlike size in one block, and what follows below. References and bounds are those
 of tests/_linear_ref.py.
 """
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -54,3 +57,19 @@ def test_rows_of_every_size_in_a_block(dtype, bits):
     o = torch.where(torch.from_numpy(near & ~np.isfinite(got)).to(DEV), 0, o)
     ref.check_o(o, np.where(near & ~np.isfinite(got), 0, ro), mo, 300, 128)
     ref.check_state(s, rs, ms, 300)
+
+
+# ------------------------------------------------------------- the kernel's text ---
+
+CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
+
+
+def test_a_group_of_four_warps_changes_its_registers_at_one_place():
+    """setmaxnreg has to be one instruction for the four warps of a group; the roles of
+    warps 8 to 11 part, so it stands before them. A run cannot show a breach."""
+    text = open(os.path.join(CSRC, "linear_tc.cuh")).read()
+    body = text[text.index("prefill_kernel("):]
+    calls = [m.start() for m in re.finditer(r"\b(give|take)_registers\(\);", body)]
+    assert len(calls) == 2
+    assert re.search(r"if \(warp >= kLoadWarp\) {\s+(//.*\s+)?give_registers\(\);\s+if \(warp == kLoadWarp\) {", body)
+    assert re.search(r"  } else {\s+take_registers\(\);.*\s+// -+ compute warps ---", body)
