@@ -1173,6 +1173,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             __stcs(reinterpret_cast<uint4*>(o + (size_t)r * p.Hv * p.dv + 8 * c),
                    *reinterpret_cast<const uint4*>(o_stage + r * 128 + ((c ^ (r & 7)) << 4)));
         }
+        fence_async_smem();   // Q's next tile comes to where these rows lay
       }
     };
 #pragma unroll 1
