@@ -801,6 +801,8 @@ gdn_status gdn_wait_selftest(int max_wait_us, void* stream) {
     return fail(GDN_ERR_INVALID_ARG, "gdn_wait_selftest: max_wait_us=%d outside [1, 1000000]", max_wait_us);
   const long long cycles = (long long)max_wait_us * 2000;   // ~2 GHz SM clock
   wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(cycles);
+  if (gdn_status s = launch_status("gdn_wait_selftest")) return s;
+  gdn::ltc::wait_selftest_kernel<<<3, 96, 0, static_cast<cudaStream_t>(stream)>>>(cycles);
   return launch_status("gdn_wait_selftest");
 }
 

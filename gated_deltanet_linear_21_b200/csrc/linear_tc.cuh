@@ -223,6 +223,16 @@ struct Wait {
         "r"(parity), "r"(dead)
         : "memory");
   }
+  // the watchdog's: for the other warps to leave
+  __device__ __forceinline__ void watch(uint64_t* left) const {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(left, 0)) {
+      if (clock64() - t0 > limit) {
+        give_up();
+        break;
+      }
+    }
+  }
   // on a flag in global memory, by one lane
   __device__ __forceinline__ void flag(const uint32_t* p, uint32_t target) const {
     if (ok() && !wait_flag_geq(p, target, limit)) give_up();
@@ -426,7 +436,7 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
 }
 
 // The scan warps: owner `ow` of 4 G carries its share of each panel's head.
-__device__ __forceinline__ void scan_role(const Params& p, int ow, int G) {
+__device__ __forceinline__ void scan_role(const Params& p, const Wait& wait, int ow, int G) {
   const int lane = threadIdx.x & 31;
   const int hl = ow / kSlices, sl = ow - hl * kSlices;
   const int seg_t = p.seg * kB;
@@ -474,8 +484,8 @@ __device__ __forceinline__ void scan_role(const Params& p, int ow, int G) {
             if (m == 0) {
               const long long now = clock64();
               if (t0 == 0) t0 = now;
-              if (__any_sync(0xffffffffu, now - t0 > p.limit)) {
-                if (lane == 0) flag_error(kErrTimeout);
+              if (__any_sync(0xffffffffu, now - t0 > p.limit || !wait.ok())) {
+                wait.give_up();
                 return;
               }
               __nanosleep(20);
@@ -843,7 +853,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       }
     } else if (warp >= kScanWarp) {
       // ------------------------------------- states between the segments ---
-      if (p.ws) scan_role(p, cta * kScanWarps + warp - kScanWarp, G);
+      if (p.ws) scan_role(p, wait, cta * kScanWarps + warp - kScanWarp, G);
     }
   } else {
     take_registers();   // waits until the others have given theirs
@@ -1311,14 +1321,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
   }
   if (warp < kWarps - 1) {
     arrive_warp(&bars[kLeft]);
-  } else {   // the watchdog
-    const long long t0 = clock64();
-    while (!mbar_try_wait(&bars[kLeft], 0)) {
-      if (clock64() - t0 > p.limit) {
-        wait.give_up();
-        break;
-      }
-    }
+  } else {
+    wait.watch(&bars[kLeft]);
   }
   tc_fence_before();
   __syncthreads();
@@ -1327,6 +1331,48 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     tmem_dealloc(tmem, 512);
   }
   if (tid == 0 && !wait.ok()) flag_error(kErrTimeout);
+}
+
+// Waits that nothing ends, one kind a CTA: on chip (CTA 0; the watchdog's time is over after
+// max_cycles), for a flag (CTA 1), the scan's for a publication (CTA 2; there the watchdog would
+// take 16 times as long, which a check of the time tells). The first warp waits on chip in all
+// of them and leaves when another gives up.
+__device__ uint32_t g_never_published[8 * kFlagWords];
+__device__ int32_t g_two_segments[2] = {0, 2 * kB};
+__global__ void __launch_bounds__(96) wait_selftest_kernel(long long max_cycles) {
+  __shared__ uint64_t bars[2];   // never completed; the warps that have left
+  __shared__ uint32_t dead;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kind = blockIdx.x;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 2);
+    fence_mbar_init();
+    dead = 0;
+  }
+  __syncthreads();
+  const long long t0 = clock64();
+  const Wait wait{smem_u32(&dead), max_cycles};
+  if (warp == 0) {
+    wait(&bars[0], 0);
+  } else if (warp == 1 && kind == 1) {
+    if (lane == 0) wait.flag(g_never_published, 1u);
+  } else if (warp == 1 && kind == 2) {
+    Params p = {};
+    p.cu_seqlens = g_two_segments;
+    p.ws = reinterpret_cast<uint8_t*>(g_never_published);
+    p.n_seqs = p.Hqk = p.Hv = p.seg = p.panel = 1;
+    p.total_T = 2 * kB;
+    p.dk = p.dv = kD;
+    p.limit = max_cycles;
+    scan_role(p, wait, 0, 8);
+  }
+  if (warp < 2) {
+    arrive_warp(&bars[1]);
+  } else {
+    Wait{smem_u32(&dead), kind == 0 ? max_cycles : 16 * max_cycles}.watch(&bars[1]);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && !wait.ok()) flag_error(clock64() - t0 > 8 * max_cycles ? kErrCheck : kErrTimeout);
 }
 
 }  // namespace ltc

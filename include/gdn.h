@@ -240,14 +240,16 @@ gdn_status gdn_decode(const void *q, const void *k, const void *v,
 
 /*
  * Diagnostic for the failure path, not part of the computation (the pages
- * have no counterpart). Enqueues one tiny kernel that runs the prefill
- * kernel's two kinds of bounded wait -- on a flag in global memory and on a
- * shared-memory mbarrier -- on objects nothing ever signals, each for about
- * max_wait_us microseconds (1 .. 1000000; ~2 GHz assumed). Both waits run out,
- * record the timeout in the device error word and return; the kernel ends
- * normally and the CUDA context stays usable. A following gdn_device_error()
- * then reports GDN_ERR_DEVICE_TIMEOUT. Returns GDN_ERR_INVALID_ARG for an
- * out-of-range max_wait_us, GDN_ERR_CUDA if the launch fails.
+ * have no counterpart). Enqueues two tiny kernels that run the prefill
+ * kernels' kinds of bounded wait on objects nothing ever signals, each for about
+ * max_wait_us microseconds (1 .. 1000000; ~2 GHz assumed): gdn_prefill's on a
+ * flag in global memory and on a shared-memory mbarrier, and gdn_linear_prefill's,
+ * which a watchdog ends, on those two and in its scan of the states. All of them
+ * run out, record the timeout in the device error word and return; the kernels
+ * end normally and the CUDA context stays usable. A following gdn_device_error()
+ * then reports GDN_ERR_DEVICE_TIMEOUT (GDN_ERR_DEVICE_CHECK if a wait was ended
+ * by the watchdog that should have ended by itself). Returns GDN_ERR_INVALID_ARG
+ * for an out-of-range max_wait_us, GDN_ERR_CUDA if a launch fails.
  */
 gdn_status gdn_wait_selftest(int max_wait_us, void *stream);
 

@@ -80,6 +80,28 @@ def test_short_blocks_leave_their_buffers_to_the_next(dtype, lo, hi):
         check(y, o[a:b], s[n:n + 1])
 
 
+# ----------------------------------------------------------------- bounded waits ---
+
+@pytest.mark.gpu
+def test_the_prefills_waits_end_by_themselves_and_the_context_survives():
+    """The waits on chip, for a flag and of the scan, which nothing ends: the kernel returns
+    within its limits (a timeout of the device; a check says that one did not end by itself)."""
+    gdn.device_error()
+    t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    t0.record()
+    gdn.wait_selftest(2000)
+    t1.record()
+    with pytest.raises(gdn.GdnError) as err:
+        gdn.device_error()
+    assert err.value.status == gdn.GDN_ERR_DEVICE_TIMEOUT
+    t1.synchronize()
+    # two waits one after the other in the first kernel (2 ms each at 2 GHz), one in the second
+    assert t0.elapsed_time(t1) > 5.0
+    gdn.device_error()
+    x = draw([1300, 40], 1, 2, 128, 128, BF16, seed=74)
+    check(x, *prefill(x))
+
+
 # ------------------------------------------------------------- the kernel's text ---
 
 CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
