@@ -521,7 +521,8 @@ gdn_status with_pool_types(gdn_code code, gdn_dtype state_dtype, int dk, F f) {
 extern "C" {
 
 size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype) {
-  if (n_seqs <= 0 || Hv <= 0 || total_T <= 0) return 0;
+  if (n_seqs <= 0 || Hv <= 0 || total_T <= 0 || total_T >= (int64_t(1) << 31) || !head_dim_ok(dk) || !head_dim_ok(dv))
+    return 0;   // (gdn_linear_prefill refuses it, or has nothing to do)
   if (!linear_on_tensor_cores(dtype, total_T)) return scan_plan(n_seqs, total_T, Hv, dk, dv).bytes;
   // sequences of one segment need none
   if (total_T <= (int64_t)linear_segment(n_seqs, total_T, Hv) * gdn::ltc::kB) return 0;

@@ -294,9 +294,10 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  *              sequence and behind the last are left as they were
  *   state_out  [n_seqs, Hv, dv, dk]  fp32 (output); may be state_in. A sequence
  *              of no tokens gets its state_in.
- *   workspace  gdn_linear_prefill_workspace_bytes() bytes, 16-byte aligned (its
- *              contents on entry do not matter). Calls that may overlap on the
- *              GPU, captured graphs among them, need workspaces of their own.
+ *   workspace  gdn_linear_prefill_workspace_bytes() bytes (0 for sizes that are
+ *              not supported), 16-byte aligned (its contents on entry do not
+ *              matter). Calls that may overlap on the GPU, captured graphs among
+ *              them, need workspaces of their own.
  *
  * o overlaps none of the inputs. scale <= 0 stands for dk^-1/2. Infinities and
  * NaN in a sequence's q, k, v or state_in stay within that sequence, but may

@@ -4,6 +4,8 @@ of tests/_linear_ref.py.
 """
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -100,6 +102,30 @@ def test_the_prefills_waits_end_by_themselves_and_the_context_survives():
     gdn.device_error()
     x = draw([1300, 40], 1, 2, 128, 128, BF16, seed=74)
     check(x, *prefill(x))
+
+
+# ------------------------------------------------------- sizes that are refused ---
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_workspace_of_sizes_that_are_not_supported(dtype):
+    """In a process of its own: no such size may end it."""
+    code = ("import torch, gated_deltanet_linear_21_b200 as gdn\n"
+            "f = lambda *a: gdn.linear_prefill_workspace_bytes(*a, dtype=torch.%s)\n"
+            "for dk, dv in ((128, 0), (0, 128), (0, 0), (128, -1), (128, -40), (96, 128), (128, 2 ** 31 - 1)):\n"
+            "    assert f(1, 4096, 4, dk, dv) == 0, (dk, dv)\n"
+            "assert f(1, 2 ** 31, 4, 128, 128) == 0 and f(1, 2 ** 62, 2 ** 31 - 1, 128, 128) == 0\n" % dtype)
+    done = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(gdn.__file__)),
+                          capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, (done.returncode, done.stderr[-500:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_heads_of_no_rows_are_refused(dtype):
+    z = lambda *shape: torch.zeros(*shape, dtype=dtype, device=DEV)  # noqa: E731
+    with pytest.raises(gdn.GdnError) as err:
+        gdn.linear_prefill(z(64, 2, 128), z(64, 2, 128), z(64, 4, 0), torch.zeros(64, 4, device=DEV))
+    assert err.value.status == gdn.GDN_ERR_UNSUPPORTED
 
 
 # ------------------------------------------------------------- the kernel's text ---
