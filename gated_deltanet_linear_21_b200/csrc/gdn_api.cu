@@ -419,6 +419,7 @@ gdn_status launch_linear_tc(const char* fn, const void* q, const void* k, const 
   if (sms < 16) return fail(GDN_ERR_CUDA, "%s: cannot query the multiprocessor count", fn);
   const int64_t items = (total_T / (prm.seg * gdn::ltc::kB) + prm.n_seqs) * prm.Hv;   // at most
   const int grid = (int)std::min<int64_t>(prm.ws ? INT64_MAX : items, std::min(sms, kLinearCtas));
+  prm.items = (int)items;
   prm.panel = std::min(prm.Hv, gdn::ltc::kScanWarps * grid / gdn::ltc::kSlices);
   if (!prm.ws) prm.panel = prm.Hv;
   // about 2 s, and ten times what the blocks take (4000 cycles each)

@@ -191,6 +191,7 @@ struct Params {
   float* state_out;
   uint8_t* ws;
   int g_stride, n_seqs, total_T, Hqk, Hv, dk, dv, seg, panel;
+  int items;           // at most, of a cu_seqlens that keeps its rules
   float scale;
   long long limit;     // SM cycles that a wait lasts at most
 };
@@ -248,9 +249,12 @@ struct Item {
 
 static_assert(sizeof(Item) * kRingItems <= 192, "shared memory budget");
 
-// Finds items in increasing order (warp-collective).
+// Finds items in increasing order (warp-collective). Sequences that overlap, as no valid
+// cu_seqlens makes them, may have more items than an int counts: the first sequence that
+// passes p.items ends the walk, and the scan's.
 struct Walk {
-  int n = 0, base = 0;
+  int n = 0;
+  long long base = 0;
   __device__ __forceinline__ bool find(const Params& p, int item, Item& it) {
     const int lane = threadIdx.x & 31;
     const int seg_t = p.seg * kB;
@@ -262,22 +266,23 @@ struct Walk {
         len = max(min(max(p.cu_seqlens[n + lane + 1], 0), p.total_T) - a, 0);
         J = max(1, (len + seg_t - 1) / seg_t);
       }
-      const int cnt = J * p.Hv;
-      int incl = cnt;
+      const long long cnt = (long long)J * p.Hv;
+      long long incl = cnt;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, off);
+        const long long x = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += x;
       }
       const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > item);
       if (hit) {
         const int src = __ffs(hit) - 1;
+        if (base + __shfl_sync(0xffffffffu, incl, src) > p.items) return false;
         n += src;
         base += __shfl_sync(0xffffffffu, incl - cnt, src);
         J = __shfl_sync(0xffffffffu, J, src);
         a = __shfl_sync(0xffffffffu, a, src);
         len = __shfl_sync(0xffffffffu, len, src);
-        const int li = item - base, per = J * p.panel, pi = li / per, rem = li - pi * per;
+        const int li = (int)(item - base), per = J * p.panel, pi = li / per, rem = li - pi * per;
         const int hp = min(p.panel, p.Hv - pi * p.panel);
         it.n = n;
         it.J = J;
@@ -453,6 +458,7 @@ __device__ __forceinline__ void scan_role(const Params& p, const Wait& wait, int
     }
     for (int i = 0; i < 32 && n0 + i < p.n_seqs; ++i) {
       const int Jn = __shfl_sync(0xffffffffu, J, i);
+      if (base + (long long)Jn * p.Hv > p.items) return;   // (as Walk)
       if (Jn > 1) {
         for (int h0 = 0; h0 < p.Hv; h0 += p.panel) {
           const int hp = min(p.panel, p.Hv - h0);
@@ -1362,6 +1368,7 @@ __global__ void __launch_bounds__(96) wait_selftest_kernel(long long max_cycles)
     p.ws = reinterpret_cast<uint8_t*>(g_never_published);
     p.n_seqs = p.Hqk = p.Hv = p.seg = p.panel = 1;
     p.total_T = 2 * kB;
+    p.items = 2;
     p.dk = p.dv = kD;
     p.limit = max_cycles;
     scan_role(p, wait, 0, 8);

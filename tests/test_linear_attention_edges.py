@@ -128,6 +128,53 @@ def test_heads_of_no_rows_are_refused(dtype):
     assert err.value.status == gdn.GDN_ERR_UNSUPPORTED
 
 
+# ------------------------------------------------- a cu_seqlens that breaks its rules ---
+
+def guarded(shape, dtype, fill):
+    """(tensor, its surroundings): a tensor inside a larger buffer of `fill`."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 2 * 8192,), fill, dtype=dtype, device=DEV)
+    return buf[8192:8192 + n].view(shape), (buf[:8192], buf[8192 + n:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("cu", [[-5, 50, 4000], [90, 20, 120], [200, 300, 400], [0, 120, 0, 120], [0, 2 ** 31 - 1],
+                                [-2 ** 31, 2 ** 31 - 1, 60], [120, 0]], ids=str)
+def test_a_broken_cu_seqlens_leaves_what_surrounds_the_arrays(dtype, cu):
+    T, Hqk, Hv, dk, dv = 120, 1, 2, 128, 128
+    x = draw([T], Hqk, Hv, dk, dv, dtype, seed=75)
+    N, fill = len(cu) - 1, 3.0
+    arrays = [guarded(t.shape, t.dtype, fill) for t in (x["q"], x["k"], x["v"], x["g"])]
+    for (t, _), n in zip(arrays, "qkvg"):
+        t.copy_(x[n])
+    arrays += [guarded((N, Hv, dv, dk), F32, fill), guarded(x["v"].shape, dtype, fill), guarded((N, Hv, dv, dk), F32, fill)]
+    need = gdn.linear_prefill_workspace_bytes(N, T, Hv, dk, dv, dtype)
+    ws, around = guarded((need,), torch.uint8, 171)
+    q, k, v, g, s0, o, s = (t for t, _ in arrays)
+    gdn.linear_prefill(q, k, v, g, s0, torch.tensor(cu, dtype=torch.int32, device=DEV), o=o, state_out=s, workspace=ws)
+    gdn.device_error()
+    for _, (a, b) in arrays:
+        assert (a == fill).all() and (b == fill).all()
+    assert (around[0] == 171).all() and (around[1] == 171).all()
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (g, "g")):
+        assert torch.equal(t.cpu(), x[n])
+    assert (s0 == fill).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_sequences_that_overlap_many_times(dtype):
+    """Far more items than the arrays' sizes allow for; with longer arrays they would pass 2^31."""
+    T, Hv, N = 20000, 8, 2000
+    z = lambda *shape, t=dtype: torch.zeros(*shape, dtype=t, device=DEV)  # noqa: E731
+    cu = torch.tensor([0, T] * N, dtype=torch.int32, device=DEV)
+    ws = torch.full((gdn.linear_prefill_workspace_bytes(2 * N - 1, T, Hv, 16, 16, dtype) + 65536,), 171, dtype=torch.uint8, device=DEV)
+    gdn.linear_prefill(z(T, 1, 16), z(T, 1, 16), z(T, Hv, 16), z(T, Hv, t=F32), None, cu, workspace=ws[:-65536])
+    gdn.device_error()
+    assert (ws[-65536:] == 171).all()
+
+
 # ------------------------------------------------------------- the kernel's text ---
 
 CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
