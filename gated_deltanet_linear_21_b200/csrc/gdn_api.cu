@@ -407,7 +407,7 @@ ScanPlan scan_plan(int n_seqs, int64_t total_T, int Hv, int dk, int dv) {
                                              : std::max(1, n_seqs / 2);
   s.seg = (int)std::min<int64_t>(std::max<int64_t>(64, (total_T / want + 16) / 16 * 16), 1 << 30);
   s.segments = total_T / s.seg + n_seqs;
-  s.decay_bytes = ((size_t)s.segments * Hv * 4 + 255) & ~size_t(255);
+  s.decay_bytes = ((size_t)s.segments * Hv * 8 + 255) & ~size_t(255);
   s.bytes = total_T <= s.seg ? 0 : s.decay_bytes + (size_t)s.segments * Hv * dv * dk * 4;
   return s;
 }
@@ -594,7 +594,7 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
   prm.state_in = state_in;
   prm.cu_seqlens = cu_seqlens;
   prm.state_out = state_out;
-  prm.decays = static_cast<float*>(workspace);
+  prm.decays = static_cast<float2*>(workspace);
   prm.states = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.decay_bytes);
   prm.g_stride = g_stride;
   prm.n_seqs = n_seqs;

@@ -7,6 +7,8 @@
 // per value head (token stride 0).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "decode.cuh"
 
@@ -119,11 +121,15 @@ decode_kernel(const TIO* __restrict__ q, const TIO* __restrict__ k, const TIO* _
 // final ones) as the running combination of those, and the outputs from them.
 //
 // Precision. exp(g_t) rounded once is off by up to 2^-24, always the same way where the
-// decay is fixed, which a thousand tokens add up to 6e-5. So the decays that are carried
-// far are exact: across segments and, in the first pass, across blocks of 16 tokens exp of
-// sums of g in fp64 (a token enters with the weight it has at its block's end); where o is
-// made the state is corrected after every block by exp of the block's sum over the product
-// of the rounded decays.
+// decay is fixed, which a thousand tokens add up to 6e-5. So decays are sums of g in fp64:
+// in the first pass a token enters with the weight it has at the end of its block of 16
+// tokens, and the state decays a block at a time; where o is made the decay of a block's last
+// token is exp of the block's sum over the product of the other rounded decays. What rounding
+// such a factor to fp32 loses goes into the next block's, so that the product of any number
+// of them is off by 2^-23 at most, and a segment's decay is held in two floats. A factor is
+// applied in the fma that adds a token: alone, s (1 - 2^-24) would always round the same way,
+// by a whole step. What is left is the rounding of the state itself, at random: 2^-25 sqrt(T)
+// relative.
 constexpr int kScanTokens = 16;   // tokens staged at a time
 constexpr int kScanThreads = 128;
 // State rows per lane, and of a CTA of 4 warps.
@@ -144,7 +150,7 @@ struct ScanParams {
   const int32_t* cu_seqlens;
   float* state_out;
   float* states;       // [segments][Hv][dv][dk]: each segment's own state, then the one that enters it
-  float* decays;       // [segments][Hv]
+  float2* decays;      // [segments][Hv]: exp of the segment's sum of g, in two parts
   int g_stride, n_seqs, total_T, Hqk, Hv, dv, seg;
   int segments;        // that the workspace has room for
   float scale;
@@ -198,7 +204,7 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
   __shared__ __align__(16) float ks[2][kScanTokens][DK];
   __shared__ __align__(16) float vs[2][kScanTokens][kScanRows];   // v, replaced by o
   __shared__ float as[2][kScanTokens];       // kOut: exp(g); else the weight of a token in the state behind the stage
-  __shared__ float fix[2];                   // kOut: what the product of the exp(g) is corrected by; else the stage's decay
+  __shared__ float stage[2];                 // !kOut: the stage's decay
   const int h = blockIdx.y, hq = h / (p.Hv / p.Hqk), dv = p.dv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane & 3, rl = warp * 8 + (lane >> 2);
@@ -223,6 +229,7 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
   }
 
   double sum = 0.0;                          // of the segment's g (warp 0)
+  double rest = 1.0;                         // what the last factor lost in rounding (warp 0)
   auto fetch = [&](int c0) {
     const int L = min(kScanTokens, it.len - c0), t0 = it.t0 + c0, b = (c0 / kScanTokens) & 1;
     for (int e = tid; e < L * (DK / 4); e += kScanThreads) {
@@ -244,15 +251,23 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
   auto decays = [&](int c0, float g) {
     const int b = (c0 / kScanTokens) & 1;
     if constexpr (kOut) {
+      const bool last = lane == min(kScanTokens, it.len - c0) - 1;
       const float a = expf(g);               // (1 behind the last token)
-      if (lane < kScanTokens) as[b][lane] = a;
-      double gs = g, prod = a;
+      double gs = g, prod = last ? 1.0 : a;
 #pragma unroll
       for (int off = kScanTokens / 2; off > 0; off >>= 1) {
         gs += __shfl_xor_sync(0xffffffffu, gs, off);
         prod *= __shfl_xor_sync(0xffffffffu, prod, off);
       }
-      if (lane == 0) fix[b] = prod > 1e-30 ? (float)(exp(gs) / prod) : 1.f;   // (below, nothing is left to correct)
+      const double want = rest * exp(gs) / prod;
+      float got = (float)want;
+      if (got > 1e-30f && got < 1e30f && prod > 1e-30) {
+        rest = want / got;
+      } else {                               // (nothing is left to correct)
+        got = a;
+        rest = 1.0;
+      }
+      if (lane < kScanTokens) as[b][lane] = last ? got : a;
     } else {
       double after = g;                      // the sum of g from this token to the stage's end, then from the next one
 #pragma unroll
@@ -261,9 +276,12 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
         if (lane + off < kScanTokens) after += x;
       }
       const double all = __shfl_sync(0xffffffffu, after, 0), next = __shfl_down_sync(0xffffffffu, after, 1);
-      const float w = (float)exp(lane == kScanTokens ? all : lane + 1 < kScanTokens ? next : 0.0);
+      double want = exp(lane == kScanTokens ? all : lane + 1 < kScanTokens ? next : 0.0);
+      if (lane == kScanTokens) want *= rest;
+      const float w = (float)want;
+      rest = w > 1e-30f && w < 1e30f ? want / w : 1.0;
       if (lane < kScanTokens) as[b][lane] = w;
-      if (lane == kScanTokens) fix[b] = w;
+      if (lane == kScanTokens) stage[b] = w;
       sum += all;
     }
   };
@@ -281,16 +299,9 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
       fetch(c0 + kScanTokens);
       if (warp == 0) g_next = gate(c0 + kScanTokens);
     }
-    const float f = fix[b];
-    if constexpr (!kOut) {
-#pragma unroll
-      for (int u = 0; u < kR; ++u) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) s[u][i] *= f;
-      }
-    }
-    for (int t = 0; t < L; ++t) {
+    auto token = [&](int t, auto first) {    // first: the one that takes the stage's decay
       const float a = as[b][t];
+      [[maybe_unused]] const float f = kOut ? 0.f : stage[b];
       float vi[kR], acc[kR][4];
 #pragma unroll
       for (int u = 0; u < kR; ++u) {
@@ -301,7 +312,7 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
         const float4 kk = *reinterpret_cast<const float4*>(&ks[b][t][4 * (sub + 4 * i)]);
-        float4 qq;
+        [[maybe_unused]] float4 qq;
         if constexpr (kOut) qq = *reinterpret_cast<const float4*>(&qs[b][t][4 * (sub + 4 * i)]);
 #pragma unroll
         for (int u = 0; u < kR; ++u) {
@@ -315,6 +326,11 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
             acc[u][1] = fmaf(x[1], qq.y, acc[u][1]);
             acc[u][2] = fmaf(x[2], qq.z, acc[u][2]);
             acc[u][3] = fmaf(x[3], qq.w, acc[u][3]);
+          } else if constexpr (decltype(first)::value) {
+            x[0] = fmaf(f, x[0], vi[u] * kk.x);
+            x[1] = fmaf(f, x[1], vi[u] * kk.y);
+            x[2] = fmaf(f, x[2], vi[u] * kk.z);
+            x[3] = fmaf(f, x[3], vi[u] * kk.w);
           } else {
             x[0] = fmaf(vi[u], kk.x, x[0]);
             x[1] = fmaf(vi[u], kk.y, x[1]);
@@ -330,14 +346,15 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
           if (sub == 0) vs[b][t][rl + 32 * u] = p.scale * r;   // only this row's lanes read v_t[row], and they have
         }
       }
+    };
+    if constexpr (kOut) {
+      for (int t = 0; t < L; ++t) token(t, std::false_type());
+    } else {
+      token(0, std::true_type());
+      for (int t = 1; t < L; ++t) token(t, std::false_type());
     }
     if (more && warp == 0) decays(c0 + kScanTokens, g_next);
     if constexpr (kOut) {
-#pragma unroll
-      for (int u = 0; u < kR; ++u) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) s[u][i] *= f;
-      }
       __syncthreads();
       for (int e = tid; e < L * (kScanRows / 4); e += kScanThreads) {
         const int t = e / (kScanRows / 4), i = 4 * (e - t * (kScanRows / 4));
@@ -357,7 +374,11 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
             make_float4(s[u][4 * i], s[u][4 * i + 1], s[u][4 * i + 2], s[u][4 * i + 3]);
     }
   }
-  if (!kOut && i0 == 0 && tid == 0) p.decays[(size_t)blockIdx.x * p.Hv + h] = (float)exp(sum);
+  if (!kOut && i0 == 0 && tid == 0) {
+    const double a = exp(sum);
+    const float hi = (float)a;
+    p.decays[(size_t)blockIdx.x * p.Hv + h] = make_float2(hi, hi < 1e30f ? (float)(a - hi) : 0.f);
+  }
 }
 
 // The states that enter the segments, in place of the segments' own, and the final ones.
@@ -385,11 +406,11 @@ combine_kernel(const ScanParams p, int per_state) {
   if (first + J > p.segments) return;   // (sequences that overlap, which no valid cu_seqlens makes)
   const size_t own = ((size_t)n * p.Hv + h) * per_state + at, step = (size_t)p.Hv * per_state;
   float* slot = p.states + ((size_t)first * p.Hv + h) * per_state + at;
-  const float* decay = p.decays + (size_t)first * p.Hv + h;
+  const float2* decay = p.decays + (size_t)first * p.Hv + h;
   float4 s = p.state_in ? *reinterpret_cast<const float4*>(p.state_in + own) : make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kAhead = 8;
   float4 x[kAhead];
-  float a[kAhead];
+  float2 a[kAhead];
   auto load = [&](int u, int j) {
     if (j < J) {
       x[u] = *reinterpret_cast<const float4*>(slot + j * step);
@@ -403,13 +424,13 @@ combine_kernel(const ScanParams p, int per_state) {
     for (int u = 0; u < kAhead; ++u) {
       if (j + u < J) {
         const float4 own_x = x[u];
-        const float own_a = a[u];
+        const float2 own_a = a[u];
         load(u, j + u + kAhead);             // in flight for eight segments' time
         *reinterpret_cast<float4*>(slot + (j + u) * step) = s;
-        s.x = fmaf(own_a, s.x, own_x.x);
-        s.y = fmaf(own_a, s.y, own_x.y);
-        s.z = fmaf(own_a, s.z, own_x.z);
-        s.w = fmaf(own_a, s.w, own_x.w);
+        s.x = fmaf(own_a.x, s.x, fmaf(own_a.y, s.x, own_x.x));
+        s.y = fmaf(own_a.x, s.y, fmaf(own_a.y, s.y, own_x.y));
+        s.z = fmaf(own_a.x, s.z, fmaf(own_a.y, s.z, own_x.z));
+        s.w = fmaf(own_a.x, s.w, fmaf(own_a.y, s.w, own_x.w));
       }
     }
   }

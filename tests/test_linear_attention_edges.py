@@ -175,6 +175,46 @@ def test_sequences_that_overlap_many_times(dtype):
     assert (ws[-65536:] == 171).all()
 
 
+# ------------------------------------------------------------- decays carried far ---
+
+def drift(lengths, Hv, dtype, seed, lo=-6.0, hi=-3.0):
+    """Largest over heads and sequences of the state's error (root of the mean square, relative)
+    with a slow decay fixed per head, where the same rounding comes back at every step. The
+    definition in closed form: S = sum_t exp(g (T - 1 - t)) v_t k_t^T in 64 bits."""
+    x = draw(lengths, 1, Hv, 16, 16, dtype, init=False, seed=seed)
+    gen = torch.Generator().manual_seed(seed)
+    x["g"] = -torch.pow(10.0, lo + (hi - lo) * torch.rand(Hv, generator=gen))
+    _, s = prefill(x)
+    got, k, v, g = ref.f64(s), ref.f64(x["k"])[:, 0], ref.f64(x["v"]), ref.f64(x["g"])
+    worst = 0.0
+    for n, T in enumerate(lengths):
+        a = int(x["cu"][n])
+        for h in range(Hv):
+            w = np.exp(g[h] * np.arange(T - 1, -1, -1))
+            want = (v[a:a + T, h] * w[:, None]).T @ k[a:a + T]
+            worst = max(worst, np.sqrt(((got[n, h] - want) ** 2).mean() / (want ** 2).mean()))
+    return worst
+
+
+# A rounding of the state is at most half a step of 2^-23 relative, 2^-23 / sqrt(12) in the root
+# of the mean square, and n of them in a row, independent, sqrt(n) times that; from a state that
+# grows from zero as sqrt(t) the sum of their squares halves. 256 elements of a head: 1.25 is 4
+# deviations.
+def rounded(n, grows=True):
+    return 1.25 * 2.0 ** -23 * (n / (24 if grows else 12)) ** 0.5
+
+
+@pytest.mark.gpu
+def test_fp32_decays_do_not_drift():
+    # unsplit, every token and every 16 tokens a rounding
+    assert drift([4096], 400, F32, 80) <= rounded(4096 * 17 / 16)
+    # two long segments and a first pass
+    assert drift([8000, 10, 10, 10], 400, F32, 81) <= rounded(8000 * 17 / 16)
+    # many segments: 144 tokens in each, 694 of them, two roundings each
+    for seed in range(82, 90):
+        assert drift([100000], 1, F32, seed, lo=-7.0, hi=-5.0) <= rounded(144 * 17 / 16 + 2 * 694, False)
+
+
 # ------------------------------------------------------------- the kernel's text ---
 
 CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
