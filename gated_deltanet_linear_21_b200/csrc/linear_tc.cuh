@@ -39,7 +39,10 @@
 // with |S| at 2^5 that is below 2^-25 of the row's largest score.
 // Log-decays are summed in fp64 (exp(G_r - G_s) of far tokens is a difference of large
 // sums) and clamped where exp is zero in fp32, so that a reset (-inf) does not turn
-// differences into NaN.
+// differences into NaN. What meets a token once -- w, rho, exp(-G_s) -- is ex2.approx of them,
+// 2^-22 relative. The decays that the state is carried with come back every block where
+// the decay is fixed, so they are exp2 in fp64: a block's rounded to fp32 (at most 8 follow
+// one another in a segment), a segment's in two floats.
 //
 // What bounds it. The data move once through HBM at 128 KB a block (fewer where heads
 // share k and q); the products' operands pass shared memory (128 bytes a cycle), which
@@ -154,7 +157,7 @@ struct Misc {
   uint32_t tmem;
   uint32_t dead;       // a wait ran out
   float gam_l;         // exp(G_L) of the block
-  float seg_gam;       // exp of the segment's total log-decay, up to this block
+  float2 seg_gam;      // exp of the segment's total log-decay, in two parts (pass A's last block)
   float w_max;         // the largest w of the block
   uint32_t steep;      // exp(-G) reaches 2^kSteep in the block
   int start_i[4];      // the log-decays (base 2) up to each quarter: whole part
@@ -177,8 +180,8 @@ constexpr int kFlagWords = 32;       // per CTA: out_ready[2], scanned[2], in_cn
 enum Flag { kOutReady = 0, kScanned = 2, kInCnt = 4, kDone = 6 };
 struct Workspace {
   __host__ __device__ static constexpr size_t flags_bytes(int ctas) { return (size_t)ctas * kFlagWords * 4; }
-  __host__ __device__ static constexpr size_t meta_offset(int ctas) { return flags_bytes(ctas); }       // float per (CTA, parity)
-  __host__ __device__ static constexpr size_t slots_offset(int ctas) { return (flags_bytes(ctas) + (size_t)ctas * 8 + 1023) & ~size_t(1023); }
+  __host__ __device__ static constexpr size_t meta_offset(int ctas) { return flags_bytes(ctas); }       // float2 per (CTA, parity)
+  __host__ __device__ static constexpr size_t slots_offset(int ctas) { return (flags_bytes(ctas) + (size_t)ctas * 16 + 1023) & ~size_t(1023); }
   // per CTA: two published states, two entering states
   __host__ __device__ static constexpr size_t bytes(int ctas) { return slots_offset(ctas) + (size_t)ctas * 4 * kStateBytes; }
 };
@@ -446,7 +449,7 @@ __device__ __forceinline__ void scan_role(const Params& p, const Wait& wait, int
   const int hl = ow / kSlices, sl = ow - hl * kSlices;
   const int seg_t = p.seg * kB;
   uint32_t* flags = reinterpret_cast<uint32_t*>(p.ws);
-  const float* meta = reinterpret_cast<const float*>(p.ws + Workspace::meta_offset(G));
+  const float2* meta = reinterpret_cast<const float2*>(p.ws + Workspace::meta_offset(G));
   uint8_t* slots = p.ws + Workspace::slots_offset(G);
   int base = 0;
   for (int n0 = 0; n0 < p.n_seqs; n0 += 32) {
@@ -499,7 +502,7 @@ __device__ __forceinline__ void scan_role(const Params& p, const Wait& wait, int
             }
             t0 = 0;
             float4 L[2][4];
-            float gam[2];
+            float2 gam[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if (x < m) {
@@ -518,10 +521,10 @@ __device__ __forceinline__ void scan_role(const Params& p, const Wait& wait, int
                 float4* to = reinterpret_cast<float4*>(slots + (size_t)(4 * cd + 2 + (rd & 1)) * kStateBytes) + 128 * sl;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                  S[u].x = fmaf(gam[x], S[u].x, L[x][u].x);
-                  S[u].y = fmaf(gam[x], S[u].y, L[x][u].y);
-                  S[u].z = fmaf(gam[x], S[u].z, L[x][u].z);
-                  S[u].w = fmaf(gam[x], S[u].w, L[x][u].w);
+                  S[u].x = fmaf(gam[x].x, S[u].x, fmaf(gam[x].y, S[u].x, L[x][u].x));
+                  S[u].y = fmaf(gam[x].x, S[u].y, fmaf(gam[x].y, S[u].y, L[x][u].y));
+                  S[u].z = fmaf(gam[x].x, S[u].z, fmaf(gam[x].y, S[u].z, L[x][u].z));
+                  S[u].w = fmaf(gam[x].x, S[u].w, fmaf(gam[x].y, S[u].w, L[x][u].w));
                   __stcg(to + 32 * u + lane, S[u]);
                 }
               }
@@ -711,7 +714,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
               }
             }
             const uint32_t steep = __any_sync(0xffffffffu, !flat);
-            const float gam_l = ex2((float)sum), seg_gam = ex2((float)seg), rest = (float)(start - whole);
+            const float rest = (float)(start - whole);
+            const double far = exp2(lane == 0 ? sum : seg);   // lane 0: the block's, lane 1: the segment's
+            const float far_hi = (float)far;
             const int whole_i = (int)whole;
             // everything is ready before the tables may be written: they are one block's
             if (cnt > 0) wait(&bars[kTabEmpty], (cnt - 1) & 1);
@@ -731,9 +736,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             if (lane == 0) {
               misc->w_max = wm;
               misc->steep = steep;
-              misc->gam_l = gam_l;
-              misc->seg_gam = seg_gam;
+              misc->gam_l = far_hi;
             }
+            // (read when the segment is published, before the next item's pass A ends)
+            if (lane == 1 && pass == 0 && b + 1 == nb)
+              misc->seg_gam = make_float2(far_hi, far_hi < 1e30f ? (float)(far - far_hi) : 0.f);
             arrive_warp(&bars[kKvFull + (cnt & 1)]);   // (the block is there when K, V and these are)
             if (pass == 1) {
               const uint32_t q = qn & 1;
@@ -869,12 +876,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     // columns of P, and of d_v in o and the state.
     const int wg = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w4) << 16) + 64 * wg;   // this warp's 64 columns of a region
-    float* meta = reinterpret_cast<float*>(p.ws + Workspace::meta_offset(G)) + 2 * cta;
+    float2* meta = reinterpret_cast<float2*>(p.ws + Workspace::meta_offset(G)) + 2 * cta;
     uint8_t* slots = p.ws + Workspace::slots_offset(G) + (size_t)cta * 4 * kStateBytes;
     uint32_t cnt = 0, qn = 0, rn = 0, phases = 0;   // phases: the parity that each barrier is waited for next
     float S[64];        // S[64 wg + i][row]
     float up = 1.f;     // f16: 2^a of this thread's row
-    float seg_gam = 1.f;
 
     auto wait_next = [&](int bar) {
       wait(&bars[bar], (phases >> (bar - kUFull)) & 1);
@@ -1232,10 +1238,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             if (a ? b >= (four ? 1 : 2) : part == 1) wait_next(kHalf + (a ? r : 0));
             if (a && !four && !here) wait_next(kHalf + (~b & 1));
             if (upd) e = put_terms(kK + s * 32768, four, part, a && r ? kColO : kColK, r);
-            if (part + 1 == parts && here && (a || four)) {
-              if (a && b + 1 == nb) seg_gam = misc->seg_gam;
-              arrive_warp(&bars[kTabEmpty]);
-            }
+            if (part + 1 == parts && here && (a || four)) arrive_warp(&bars[kTabEmpty]);
             if (a || part == 1) continue;
             if (!a && b == 0) {
               // the state that enters
@@ -1305,7 +1308,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
 #pragma unroll
           for (int v = 0; v < 16; ++v)
             __stcg(out + 256 * v + tid, make_float4(S[4 * v], S[4 * v + 1], S[4 * v + 2], S[4 * v + 3]));
-          if (tid == 0) __stcg(meta + par, seg_gam);
+          if (tid == 0) __stcg(meta + par, misc->seg_gam);
           arrive_warp(&bars[kPub]);
         }
       }

@@ -215,6 +215,19 @@ def test_fp32_decays_do_not_drift():
         assert drift([100000], 1, F32, seed, lo=-7.0, hi=-5.0) <= rounded(144 * 17 / 16 + 2 * 694, False)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_decays_do_not_drift_on_the_tensor_cores(dtype):
+    """196 segments of 8 blocks: two roundings for each that the state passes, and each
+    block's own part: its products, 4 terms x 8 steps added in fp32, each off by at most 2^-24 of
+    what is there (2^-23 where the unit cuts off instead of rounding: 2^-23 x 32 / 2 on
+    average over a growing sum, times 1 / sqrt(12) where the signs differ), the terms' 2^-22 and
+    the weights' 2^-22."""
+    own = 2.0 ** -23 * 16 / 12 ** 0.5 + 2 * 2.0 ** -22
+    for seed in range(90, 98):
+        assert drift([200000], 1, dtype, seed, lo=-7.0, hi=-5.0) <= rounded(2 * 196 + 8, False) + own
+
+
 # ------------------------------------------------------------- the kernel's text ---
 
 CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
