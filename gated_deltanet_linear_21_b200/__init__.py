@@ -371,8 +371,9 @@ def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=
     g_stride = _decay(g, T, Hv, device)
     f32 = torch.float32
     with _running_on(device, stream):
-        if cu_seqlens is None:
-            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=device)
+        if cu_seqlens is None:   # filled on the device: no copy from the host, which a graph could not capture
+            cu_seqlens = torch.zeros(2, dtype=torch.int32, device=device)
+            cu_seqlens[1:].fill_(T)
         elif not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 and cu_seqlens.numel() > 0
                   and _fits(cu_seqlens, torch.int32, cu_seqlens.shape, device)):
             _dev(cu_seqlens, "cu_seqlens", torch.int32)

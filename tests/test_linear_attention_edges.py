@@ -104,6 +104,33 @@ def test_the_prefills_waits_end_by_themselves_and_the_context_survives():
     check(x, *prefill(x))
 
 
+# ------------------------------------------------------------ one prompt, no offsets ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [0, 1, 200, 1500])
+def test_one_prompt_without_cu_seqlens_captured_and_on_another_stream(dtype, T):
+    x = draw([T], 1, 2, 128, 128, dtype, seed=76)
+    d = {n: t.to(DEV) for n, t in x.items()}
+    args = (d["q"], d["k"], d["v"], d["g"], d["state_in"])
+    want = gdn.linear_prefill(*args, d["cu"])
+    assert all(torch.equal(a, b) for a, b in zip(gdn.linear_prefill(*args), want))
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = gdn.linear_prefill(*args, stream=other)
+    other.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = gdn.linear_prefill(*args)
+    for t in got:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    gdn.device_error()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ------------------------------------------------------- sizes that are refused ---
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
