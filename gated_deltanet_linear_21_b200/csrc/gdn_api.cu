@@ -567,6 +567,9 @@ gdn_status gdn_linear_prefill(const void* q, const void* k, const void* v, const
       return fail(GDN_ERR_UNSUPPORTED, "%s: %d sequences, %lld tokens, %d heads are more than this kernel schedules", fn,
                   n_seqs, (long long)total_T, Hv);
     gdn::ltc::Params prm = {};
+    prm.q = q;
+    prm.k = k;
+    prm.v = v;
     prm.g = g;
     prm.state_in = state_in;
     prm.cu_seqlens = cu_seqlens;

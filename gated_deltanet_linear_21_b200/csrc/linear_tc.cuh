@@ -44,6 +44,12 @@
 // the decay is fixed, so they are exp2 in fp64: a block's rounded to fp32 (at most 8 follow
 // one another in a segment), a segment's in two floats.
 //
+// Infinities and NaN. Scores above the diagonal are zeros, and zero times a NaN of V is one: it
+// reaches the rows of its column in front of its token, as far as the block goes. It also
+// stays in the state (in what a segment adds to it, where that is looked at), so one look an
+// item finds it, and those rows are then made again, token by token, from the state that
+// entered.
+//
 // What bounds it. The data move once through HBM at 128 KB a block (fewer where heads
 // share k and q); the products' operands pass shared memory (128 bytes a cycle), which
 // is the tighter bound. So K~'s terms and P are tensor-memory operands: K~ is read from
@@ -147,7 +153,9 @@ constexpr int kRingItems = 4;
 // before all of them have seen the first: each next completion has to need something that
 // they do after that wait. Hence two barriers for pass A's two accumulators (kUFull,
 // kURead) and four, as many as there are ring items, for kGot: the courier may fall behind
-// the compute warps by that many and hands its item back after it.
+// the compute warps by that many and hands its item back after it. kGot is also what keeps
+// the courier from the next kInReady and kOutOk until all warps have seen this item's: they
+// arrive on it after those waits.
 enum Bar { kKvFull = 0, kKvEmpty = 2, kItFull = 4, kItEmpty = 8, kGot = 12, kUFull = 16, kURead = 18, kKt = 20, kHalf = 22,
            kQFull = 24, kQFree = 26, kTabEmpty = 28, kPFull, kSReady, kOFull, kSlotFree, kPub, kInReady, kOutOk, kCBar,
            kLeft, kNumBars };
@@ -187,6 +195,7 @@ struct Workspace {
 };
 
 struct Params {
+  const void *q, *k, *v;
   const float* g;
   const float* state_in;
   const int32_t* cu_seqlens;
@@ -683,7 +692,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
               const double y = __shfl_up_sync(0xffffffffu, incl, off);
               if (lane >= off) incl += y;
             }
-            const double sum = __shfl_sync(0xffffffffu, incl, 31), before = incl - c[3];
+            const double sum = __shfl_sync(0xffffffffu, incl, 31), up = __shfl_up_sync(0xffffffffu, incl, 1);
+            const double before = lane > 0 ? up : 0.0;   // (not incl - c[3], which a NaN or +inf of this lane would be)
             const double start = __shfl_sync(0xffffffffu, before, lane & 24), whole = floor(start);
             seg += sum;
             float w[4], wm = 0.f;
@@ -851,15 +861,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             if (lane == 0) wait.flag(flags + kInCnt + par, kSlices * use);
             arrive_warp(&bars[kInReady]);
           }
-          wait(&bars[kGot + (i & 3)], (i >> 2) & 1);
-          if (lane == 0) {
-            fence_acq_rel_gpu();
-            st_relaxed_gpu(flags + kDone, i + 1);
-          }
           if (last && it.J > 1) {
             // state_out may be state_in, whose reader is then the first segment
             if (lane == 0) wait.flag(all + (it.first % G) * kFlagWords + kDone, it.first / G + 1);
             arrive_warp(&bars[kOutOk]);
+          }
+          wait(&bars[kGot + (i & 3)], (i >> 2) & 1);
+          if (lane == 0) {
+            fence_acq_rel_gpu();
+            st_relaxed_gpu(flags + kDone, i + 1);
           }
           arrive_warp(&bars[kItEmpty + (i & 3)]);
         }
@@ -881,6 +891,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
     uint32_t cnt = 0, qn = 0, rn = 0, phases = 0;   // phases: the parity that each barrier is waited for next
     float S[64];        // S[64 wg + i][row]
     float up = 1.f;     // f16: 2^a of this thread's row
+    bool bad = false;   // infinities or NaN in this warp's part of what the item adds to the state
 
     auto wait_next = [&](int bar) {
       wait(&bars[bar], (phases >> (bar - kUFull)) & 1);
@@ -1198,10 +1209,73 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         fence_async_smem();   // Q's next tile comes to where these rows lay
       }
     };
+    auto not_finite = [&] {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 64; ++i) t[i & 3] = fmaf(S[i], 0.f, t[i & 3]);
+      return __any_sync(0xffffffffu, !((t[0] + t[1]) + (t[2] + t[3]) == 0.f)) != 0;
+    };
+    // Rows of this warp in front of a column's first infinity or NaN in V, in its block: again, by
+    // the recurrence, with four of d_k to a lane. A column's NaN is in the state of all four warps
+    // that hold it, so each finds its own rows.
+    auto mend_rows = [&](int par) {
+      if (lane == 0) bulk_wait_all();   // the rows' own way out is over
+      __syncwarp();
+      const int hq = it.h / (p.Hv / p.Hqk), cols = min(64, p.dv - 64 * wg);
+      const T* const q = static_cast<const T*>(p.q) + ((size_t)it.t0 * p.Hqk + hq) * p.dk;
+      const T* const k = static_cast<const T*>(p.k) + ((size_t)it.t0 * p.Hqk + hq) * p.dk;
+      const size_t at_v = ((size_t)it.t0 * p.Hv + it.h) * p.dv + 64 * wg, step = (size_t)p.Hv * p.dv;
+      const T* const v = static_cast<const T*>(p.v) + at_v;
+      T* const o = static_cast<T*>(p.o) + at_v;
+      int first[2] = {it.len, it.len};   // of columns 2 lane, 2 lane + 1
+      if (2 * lane < cols) {
+#pragma unroll 4
+        for (int t = it.len - 1; t >= 0; --t) {
+          const float2 x = Op16<T>::unpack2(*reinterpret_cast<const uint32_t*>(v + t * step + 2 * lane));
+          if (!(fabsf(x.x) < kInf)) first[0] = t;
+          if (!(fabsf(x.y) < kInf)) first[1] = t;
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < cols; ++c) {
+        const int end = __shfl_sync(0xffffffffu, c & 1 ? first[1] : first[0], c >> 1);
+        const int lo = (end & ~(kB - 1)) + 32 * w4, hi = min(lo + 32, end);
+        if (end == it.len || lo >= hi) continue;
+        float s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j = 32 * u + lane;
+          s[u] = 0.f;
+          if (it.j > 0)
+            s[u] = __ldcg(reinterpret_cast<const float*>(slots + (size_t)(2 + par) * kStateBytes) +
+                          ((size_t)(c >> 2) * 256 + 128 * wg + j) * 4 + (c & 3));
+          else if (p.state_in && j < p.dk)
+            s[u] = __ldcs(p.state_in + (((size_t)it.n * p.Hv + it.h) * p.dv + 64 * wg + c) * p.dk + j);
+        }
+#pragma unroll 1
+        for (int t = 0; t < hi; ++t) {
+          const float a = expf(p.g[(size_t)(it.t0 + t) * p.g_stride + it.h]), x = to_f32(v[t * step + c]);
+          float r = 0.f;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int j = 32 * u + lane;
+            if (j >= p.dk) continue;
+            s[u] = fmaf(a, s[u], x * to_f32(k[(size_t)t * p.Hqk * p.dk + j]));
+            if (t >= lo) r = fmaf(s[u], to_f32(q[(size_t)t * p.Hqk * p.dk + j]), r);
+          }
+          if (t >= lo) {
+            r = group_sum<32>(r);
+            if (lane == 0) o[t * step + c] = from_f32<T>(p.scale * r);
+          }
+        }
+      }
+      __syncwarp();
+    };
 #pragma unroll 1
     for (uint32_t i = 0; next_item(i, it); ++i) {
       const int nb = (it.len + kB - 1) / kB, par = i & 1;
       const bool last = it.j + 1 == it.J;
+      bad = false;
       // One body for both passes. K~ of a block is made while the tensor core is at the block
       // before it: in pass A the state follows a block behind; in pass B o of the block before
       // leaves tensor memory first, because K~ goes where it was.
@@ -1289,7 +1363,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
                 send_o(o_stage, it.t0 + (b - 1) * kB, it.h, min(kB, it.len - (b - 1) * kB));
               }
               if (here) write_copy(down);
-              if (p.ws && b == 0) arrive_warp(&bars[kGot + (i & 3)]);
+              if (p.ws && b == 0 && !last && !bad) arrive_warp(&bars[kGot + (i & 3)]);
             }
           }
           if (!a) {
@@ -1303,6 +1377,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           if (a ? b > 0 : upd) update_state(a ? ~b & 1 : 0, a ? gam_before : gam, pow2i(a ? -e_before : -e));
         }
         if (pass == 0) {
+          bad = not_finite();
           wait_next(kSlotFree);
           float4* out = reinterpret_cast<float4*>(slots + (size_t)par * kStateBytes);
 #pragma unroll
@@ -1312,9 +1387,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
           arrive_warp(&bars[kPub]);
         }
       }
+      if (last) bad = not_finite();
+      if (bad && wait.ok()) {
+        // (S waits in tensor memory, where the state's products are over)
+        const uint32_t* const u = reinterpret_cast<const uint32_t*>(S);
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) tmem_st16(tl + kColU + c, u + c);
+        tmem_wait_st();
+        mend_rows(par);
+        tmem_ld64(tl + kColU, S);
+      }
+      // The state that entered is needed no more; nor does the next item's kOutOk come before this.
+      if (last && it.J > 1) wait_next(kOutOk);
+      if (p.ws && (last || bad)) arrive_warp(&bars[kGot + (i & 3)]);
       if (last) {
-        // the state after the sequence: a row of 32 consecutive columns a store
-        if (it.J > 1) wait_next(kOutOk);
+        // the state after the sequence: a row of 32 consecutive columns a store. Where it takes
+        // the place of state_in, no warp reads that any more.
+        if (it.J == 1 && p.state_in == p.state_out) sync();
         float* out = p.state_out + (((size_t)it.n * p.Hv + it.h) * p.dv + 64 * wg) * p.dk + row;
         if (kWhole) {
 #pragma unroll

@@ -300,9 +300,11 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  *              them, need workspaces of their own.
  *
  * o overlaps none of the inputs. scale <= 0 stands for dk^-1/2. Infinities and
- * NaN in a sequence's q, k, v or state_in stay within that sequence, but may
- * reach rows of o up to 127 tokens before the one that holds them. A bounded
- * wait that ran out is reported by gdn_device_error.
+ * NaN reach what the recurrence takes them to (their token's row and later ones
+ * of their sequence, and of o and the state only the channels that depend on
+ * them), where an infinity may come out as NaN. For bf16 and f16 a block of
+ * tokens that holds some in v takes longer. A bounded wait that ran out is
+ * reported by gdn_device_error.
  *
  * Supported: every dtype, dk and dv in {16, 32, 64, 128}; n_seqs and Hv up to
  * 65535. State and sums are fp32. For bf16 and f16 the state that meets q and

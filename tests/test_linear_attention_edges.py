@@ -131,6 +131,65 @@ def test_one_prompt_without_cu_seqlens_captured_and_on_another_stream(dtype, T):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+# ------------------------------------------------------------- infinities and NaN ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("what", ["v", "k", "q", "g"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lengths", [[300, 40], [1400, 130]], ids=str)
+def test_a_bad_token_reaches_what_the_definition_says(dtype, what, bad, lengths):
+    """NaN and infinities in single channels: the rows before their token, and channels of
+    v that they are not in, keep their values; all that depends on them is infinite or NaN."""
+    if what == "g" and bad != bad or what == "g" and bad < 0:
+        bad = float("nan")                                # (-inf is a reset, tested elsewhere)
+    for at in ([(5, 0, 3), (130, 1, 70)], [(127, 1, 127), (128, 0, 0)], [(lengths[0] - 1, 0, 64), (lengths[0] + 30, 1, 9)],
+               [(0, 0, 1), (lengths[0] // 2, 0, 2), (lengths[0] // 2 - 1, 1, 2)]):
+        x = draw(lengths, 2, 2, 128, 128, dtype, seed=77)
+        clean, poison = dict(x), dict(x)
+        for y, z in ((x, bad), (clean, 0.0), (poison, float("nan"))):
+            y[what] = y[what].clone()
+            for t, h, c in at:
+                y[what][(t, h, c)[:y[what].dim()]] = z
+        o, s = prefill(x)
+        reached = ref.linear_prefill(*(poison[n] for n in ("q", "k", "v", "g", "state_in", "cu")))[:2]
+        ro, rs, mo, ms = ref.linear_prefill(*(clean[n] for n in ("q", "k", "v", "g", "state_in", "cu")))
+        for got, mask, r, m, check_it in ((o, ~np.isfinite(reached[0]), ro, mo, lambda *a: ref.check_o(*a, max(lengths), 128)),
+                                          (s, ~np.isfinite(reached[1]), rs, ms, lambda *a: ref.check_state(*a, max(lengths)))):
+            mask_t = torch.from_numpy(mask).to(DEV)
+            assert (mask.any() or (what == "q" and got is s)) and not torch.isfinite(got[mask_t]).any()
+            check_it(got.masked_fill(mask_t, 0), np.where(mask, 0, r), np.where(mask, 0, m))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (16, 32), (64, 16)])
+def test_many_bad_channels_with_the_state_in_place(dtype, dk, dv):
+    """Rows in front of bad tokens are made again from the entering state, which the call
+    overwrites: sequences of one segment and of several, every third channel bad."""
+    lengths = [100, 1500, 0, 60, 200]
+    x = draw(lengths, 1, 2, dk, dv, dtype, seed=78)
+    cu = x["cu"].tolist()
+    clean, poison = dict(x), dict(x)
+    for y, z in ((x, float("inf")), (clean, 0.0), (poison, float("nan"))):
+        y["v"] = y["v"].clone()
+        for c in range(0, dv, 3):
+            for n in (0, 1, 1, 4):
+                y["v"][cu[n] + (37 * c + 11 * n) % lengths[n], c % 2, c] = z
+            y["v"][cu[1] + 1030 + c, 1, c] = z
+    d = {n: t.to(DEV) for n, t in x.items()}
+    o = torch.full(x["v"].shape, 7.0, dtype=dtype, device=DEV)
+    _, s = gdn.linear_prefill(d["q"], d["k"], d["v"], d["g"], d["state_in"], d["cu"], o=o, state_out=d["state_in"])
+    gdn.device_error()
+    reached = ref.linear_prefill(*(poison[n] for n in ("q", "k", "v", "g", "state_in", "cu")))[:2]
+    ro, rs, mo, ms = ref.linear_prefill(*(clean[n] for n in ("q", "k", "v", "g", "state_in", "cu")))
+    for got, mask, r, m, check_it in ((o, ~np.isfinite(reached[0]), ro, mo, lambda *a: ref.check_o(*a, 1500, dk)),
+                                      (s, ~np.isfinite(reached[1]), rs, ms, lambda *a: ref.check_state(*a, 1500))):
+        mask_t = torch.from_numpy(mask).to(DEV)
+        assert mask.any() and not torch.isfinite(got[mask_t]).any()
+        check_it(got.masked_fill(mask_t, 0), np.where(mask, 0, r), np.where(mask, 0, m))
+
+
 # ------------------------------------------------------- sizes that are refused ---
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
