@@ -211,6 +211,9 @@ scan_kernel(const float* __restrict__ q, const float* __restrict__ k, const floa
   const int i0 = blockIdx.z * kScanRows, row = i0 + rl;
   Segment it;
   if (!find_segment(p, blockIdx.x, it)) return;
+  if (!GDN_CHECK(it.n < p.n_seqs && it.j >= 0 && it.j < it.J && it.t0 >= 0 && it.len >= 0 && it.t0 + it.len <= p.total_T &&
+                 (int)blockIdx.x < p.segments))
+    return;
   if (!kOut && it.J == 1) return;            // nothing to combine
 
   // row 32 u further on: u * 32 * DK words
@@ -404,6 +407,7 @@ combine_kernel(const ScanParams p, int per_state) {
   first -= J;
   if (J == 1 || at >= per_state) return;
   if (first + J > p.segments) return;   // (sequences that overlap, which no valid cu_seqlens makes)
+  if (!GDN_CHECK(first >= 0 && J > 0 && n < p.n_seqs)) return;
   const size_t own = ((size_t)n * p.Hv + h) * per_state + at, step = (size_t)p.Hv * per_state;
   float* slot = p.states + ((size_t)first * p.Hv + h) * per_state + at;
   const float2* decay = p.decays + (size_t)first * p.Hv + h;

@@ -495,7 +495,7 @@ __device__ __forceinline__ void scan_role(const Params& p, const Wait& wait, int
             const int at = lane < 2 ? item : item + hp, c = at % G, r = at / G;
             const uint32_t need = lane < 2 ? r + 1 : max(r - 1, 0);
             bool ready = false;
-            if (lane < 4 && jl + 1 < Jn)
+            if (lane < 4 && jl + 1 < Jn && GDN_CHECK(item >= 0 && at < p.items))
               ready = ld_acquire_gpu(flags + c * kFlagWords + (lane < 2 ? kOutReady + (r & 1) : kDone)) >= need;
             const uint32_t bits = __ballot_sync(0xffffffffu, ready);
             const int m = (bits & 5u) != 5u ? 0 : (bits & 10u) != 10u ? 1 : 2;
@@ -624,6 +624,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       bool more = true;
       for (uint32_t i = 0; more && wait.ok(); ++i) {
         more = walk.find(p, cta + (int)i * G, it);
+        if (more) more = GDN_CHECK(it.n < p.n_seqs && it.h >= 0 && it.h < p.Hv && it.j >= 0 && it.j < it.J && it.len >= 0 &&
+                                   it.t0 >= 0 && it.t0 + it.len <= p.total_T && it.first >= 0 && it.first < p.items &&
+                                   (p.ws || it.J == 1));
         if (!more) it.n = -1;
         if (i >= kRingItems) wait(&bars[kItEmpty + (i & 3)], ((i >> 2) - 1) & 1);
         if (lane == 0) ring[i & 3] = it;

@@ -106,6 +106,7 @@ store_kernel(const TS* __restrict__ state, const int32_t* __restrict__ slots, in
   for (int j = i + 1 + (int)threadIdx.x; j < n; j += kThreads) later |= slots[j] == slot;
   if (__syncthreads_or(later)) return;
 
+  if (!GDN_CHECK(i < n && tile < tiles && (long long)tile * kTile < per_state)) return;
   const long long base = (long long)tile * kTile + threadIdx.x * 4;
   const TS* src = state + (size_t)i * per_state;
   float4 x[kUnroll];
@@ -142,6 +143,7 @@ load_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ exps
   const int i = blockIdx.x / tiles, tile = blockIdx.x - i * tiles;
   const int slot = slots[i];
   const bool held = slot >= 0 && slot < n_slots;   // another slot: a sequence without a past, zeros
+  if (!GDN_CHECK(tile < tiles && (long long)tile * kTile < per_state)) return;
   const long long base = (long long)tile * kTile + threadIdx.x * 4;
   const uint32_t* csrc = codes + (size_t)(held ? slot : 0) * (per_state / 4);
   const uint8_t* esrc = exps + (size_t)(held ? slot : 0) * (per_state / (4 * G));

@@ -384,7 +384,8 @@ gdn_status gdn_device_error(void *stream);
  * 1 if this library was built with GDN_DEBUG (libgdn_debug.so), else 0. The
  * debug build checks, on the device, the ring positions and slots, sequence
  * bounds, token and head coordinates and state offsets that the tensor-core
- * prefill computes before it uses them; a failed check records
+ * prefill computes before it uses them, the items, segments and slots of
+ * gdn_linear_prefill and the tiles of the state pool; a failed check records
  * GDN_ERR_DEVICE_CHECK in the device error word and stops that CTA's work
  * (the waits of the others are bounded), instead of reading or writing out
  * of bounds. It never traps. Diagnostic only: the checks cost time, and the

@@ -17,6 +17,7 @@ from tests.test_linear_attention import check, draw, prefill
 gdn = pytest.importorskip("gated_deltanet_linear_21_b200")
 
 DEV = "cuda"
+CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 
@@ -190,6 +191,67 @@ def test_many_bad_channels_with_the_state_in_place(dtype, dk, dv):
         check_it(got.masked_fill(mask_t, 0), np.where(mask, 0, r), np.where(mask, 0, m))
 
 
+# ------------------------------------------------------------------ the debug build ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("lengths,Hqk,Hv", [([1], 1, 1), ([700, 0, 1500, 33], 2, 4), ([0, 3] * 60 + [1300], 2, 40)], ids=str)
+def test_the_debug_build_checks_the_prefill_and_gives_the_same_bits(dtype, lengths, Hqk, Hv):
+    lib = gdn.debug_lib()
+    x = draw(lengths, Hqk, Hv, 64, 64, dtype, seed=79)
+    want = prefill(x)
+    d = {n: t.to(DEV) for n, t in x.items()}
+    T, N = x["q"].shape[0], len(lengths)
+    code = {BF16: gdn.GDN_BF16, F16: gdn.GDN_F16, F32: gdn.GDN_F32}[dtype]
+    o, s = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+    need = lib.gdn_linear_prefill_workspace_bytes(N, T, Hv, 64, 64, code)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.gdn_linear_prefill(d["q"].data_ptr(), d["k"].data_ptr(), d["v"].data_ptr(), d["g"].data_ptr(), Hv,
+                                  d["state_in"].data_ptr(), d["cu"].data_ptr(), N, T, Hqk, Hv, 64, 64, 0.0, code,
+                                  o.data_ptr(), s.data_ptr(), ws.data_ptr(), need, st) == gdn.GDN_OK
+    assert lib.gdn_device_error(st) == gdn.GDN_OK, lib.gdn_last_error().decode()
+    assert torch.equal(o, want[0]) and torch.equal(s, want[1])
+
+
+@pytest.mark.gpu
+def test_the_debug_build_checks_the_pool():
+    lib = gdn.debug_lib()
+    x = torch.randn(5, 3, 128, 64, device=DEV)
+    codes, exps = gdn.state_pool(4, 3, 128, 64)
+    slots = torch.tensor([3, -1, 0, 9, 1], dtype=torch.int32, device=DEV)
+    out, st = torch.empty_like(x), torch.cuda.current_stream().cuda_stream
+    a = (slots.data_ptr(), 5, 4, 3, 64, 128, 0)
+    assert lib.gdn_state_store(x.data_ptr(), gdn.GDN_F32, *a, codes.data_ptr(), exps.data_ptr(), st) == gdn.GDN_OK
+    assert lib.gdn_state_load(codes.data_ptr(), exps.data_ptr(), *a, out.data_ptr(), gdn.GDN_F32, st) == gdn.GDN_OK
+    assert lib.gdn_device_error(st) == gdn.GDN_OK, lib.gdn_last_error().decode()
+    assert torch.equal(out, gdn.state_load(codes, exps, slots))
+
+
+def test_the_kernels_hold_index_checks():
+    """What the headers say of the debug build: a check in every kernel that works with indices from the device."""
+    for name, kernels in (("linear_tc.cuh", 2), ("linear.cuh", 2), ("state_pool.cuh", 2)):
+        assert open(os.path.join(CSRC, name)).read().count("GDN_CHECK(") >= kernels, name
+
+
+# ------------------------------------------------------- many calls, few segments ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_last_segments_that_follow_one_another_on_a_cta(dtype):
+    """Sequences of two segments, more of them than CTAs: a CTA's items are last ones in a row, whose
+    flags come early. A wait that missed its turn would run out."""
+    x = draw([1100, 1300] * 12, 4, 32, 128, 128, dtype, init=False, seed=85)
+    d = {n: t.to(DEV) if t is not None else None for n, t in x.items()}
+    state = torch.randn(24, 32, 128, 128, device=DEV)
+    first = gdn.linear_prefill(d["q"], d["k"], d["v"], d["g"], state, d["cu"])
+    for i in range(150):
+        got = gdn.linear_prefill(d["q"], d["k"], d["v"], d["g"], state, d["cu"])
+        if i % 10 == 0:
+            assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    gdn.device_error()
+
+
 # ------------------------------------------------------- sizes that are refused ---
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
@@ -315,9 +377,6 @@ def test_decays_do_not_drift_on_the_tensor_cores(dtype):
 
 
 # ------------------------------------------------------------- the kernel's text ---
-
-CSRC = os.path.join(os.path.dirname(gdn.__file__), "csrc")
-
 
 def test_a_group_of_four_warps_changes_its_registers_at_one_place():
     """setmaxnreg has to be one instruction for the four warps of a group; the roles of
