@@ -132,6 +132,29 @@ def test_one_prompt_without_cu_seqlens_captured_and_on_another_stream(dtype, T):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T", [2500, 4096])
+def test_errors_in_the_mean_square_with_a_slow_decay(dtype, T):
+    """What bounds for single elements, which grow with T, let pass: a dropped term of K, or a
+    decay that drifts. The state: at most 64 tokens (fp32) or 8 blocks in a row, then T / 64
+    segments of two roundings, and the products' part as in the test above. o in 16 bits: its
+    own rounding, at most u / sqrt(3) in the mean square, and independent of it the same of
+    every term (one operand of each is rounded); in fp32 the state's, and of a sum of 128
+    terms 12 roundings in a row (8 fma, 4 additions)."""
+    x = draw([T], 1, 2, 128, 128, dtype, init=False, seed=86)
+    x["g"] = torch.tensor([-3e-4, -2e-5])
+    o, s = prefill(x)
+    ro, rs, _, _ = ref.linear_prefill(x["q"], x["k"], x["v"], x["g"], None, x["cu"])
+    rms = lambda got, want: np.sqrt(((ref.f64(got) - want) ** 2).mean((0, 2)) / (want ** 2).mean((0, 2))).max()  # noqa: E731
+    state = rounded(64 * 17 / 16 + 2 * T / 64, False)
+    if dtype != F32:
+        state += 2.0 ** -23 * 16 / 12 ** 0.5 + 2 * 2.0 ** -22
+    assert rms(s[0].transpose(0, 1), rs[0].transpose(1, 0, 2)) <= state      # [dv, heads, dk]
+    u = torch.finfo(dtype).eps / 2
+    assert rms(o, ro) <= (u * (2 / 3) ** 0.5 if dtype != F32 else state + rounded(12, False))
+
+
 # ------------------------------------------------------------- infinities and NaN ---
 
 @pytest.mark.gpu
