@@ -359,7 +359,7 @@ def linear_prefill_workspace_bytes(n_seqs, total_T, Hv, dk, dv, dtype=torch.bflo
 def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=None, state_out=None,
                    workspace=None, stream=None):
     """Decayed linear attention over packed sequences: S_t = exp(g_t) S_{t-1} +
-    v_t k_t^T, o_t = scale S_t q_t (scale None: dk^-1/2).
+    v_t k_t^T, o_t = scale S_t q_t (scale None, zero or negative: dk^-1/2).
 
     q, k [T, Hqk, dk]; v [T, Hv, dv] (bf16, f16 or fp32, same dtype); g fp32
     [T, Hv], or [Hv] for a decay fixed per value head; state_in [N, Hv, dv, dk]
@@ -372,8 +372,8 @@ def linear_prefill(q, k, v, g, state_in=None, cu_seqlens=None, *, scale=None, o=
     f32 = torch.float32
     with _running_on(device, stream):
         if cu_seqlens is None:   # filled on the device: no copy from the host, which a graph could not capture
-            cu_seqlens = torch.zeros(2, dtype=torch.int32, device=device)
-            cu_seqlens[1:].fill_(T)
+            cu_seqlens = torch.arange(0, T + 1, T, dtype=torch.int32, device=device) if T > 0 else \
+                torch.zeros(2, dtype=torch.int32, device=device)
         elif not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 and cu_seqlens.numel() > 0
                   and _fits(cu_seqlens, torch.int32, cu_seqlens.shape, device)):
             _dev(cu_seqlens, "cu_seqlens", torch.int32)
