@@ -1391,7 +1391,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
         }
       }
       if (last) bad = not_finite();
-      if (bad && wait.ok()) {
+      if (bad) {
         // (S waits in tensor memory, where the state's products are over)
         const uint32_t* const u = reinterpret_cast<const uint32_t*>(S);
 #pragma unroll

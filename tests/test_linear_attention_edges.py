@@ -214,6 +214,27 @@ def test_many_bad_channels_with_the_state_in_place(dtype, dk, dv):
         check_it(got.masked_fill(mask_t, 0), np.where(mask, 0, r), np.where(mask, 0, m))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+def test_a_bad_element_of_the_entering_state(dtype, bad):
+    lengths = [1400, 0, 130]
+    x = draw(lengths, 2, 2, 128, 128, dtype, seed=87)
+    clean, poison = dict(x), dict(x)
+    for y, z in ((x, bad), (clean, 0.0), (poison, float("nan"))):
+        y["state_in"] = y["state_in"].clone()
+        for at in ((0, 0, 5, 77), (0, 1, 100, 0), (1, 0, 3, 3), (2, 1, 127, 127)):
+            y["state_in"][at] = z
+    o, s = prefill(x)
+    reached = ref.linear_prefill(*(poison[n] for n in ("q", "k", "v", "g", "state_in", "cu")))[:2]
+    ro, rs, mo, ms = ref.linear_prefill(*(clean[n] for n in ("q", "k", "v", "g", "state_in", "cu")))
+    for got, mask, r, m, check_it in ((o, ~np.isfinite(reached[0]), ro, mo, lambda *a: ref.check_o(*a, 1400, 128)),
+                                      (s, ~np.isfinite(reached[1]), rs, ms, lambda *a: ref.check_state(*a, 1400))):
+        mask_t = torch.from_numpy(mask).to(DEV)
+        assert mask.any() and not torch.isfinite(got[mask_t]).any()
+        check_it(got.masked_fill(mask_t, 0), np.where(mask, 0, r), np.where(mask, 0, m))
+
+
 # ------------------------------------------------------------------ the debug build ---
 
 @pytest.mark.gpu
