@@ -377,9 +377,9 @@ bool linear_on_tensor_cores(gdn_dtype dtype, int64_t total_T) { return dtype != 
 
 // Blocks of 128 tokens per segment. Fewer make more items, so that one sequence's
 // heads fill the GPU and unequal sequences even out; more make fewer hand-overs of a
-// state: eight packed sequences of 32 heads take 438 us with up to 8, 456 with up to 4 and
-// 447 with up to 12 (32768 tokens: 469, 487 and 484). The lengths are on the device: only
-// their mean is known here.
+// state: eight packed sequences of 32 heads take 436 us with up to 8, 458 with up to 4 and
+// 447 with up to 12 (32768 tokens, f16: 500, 521 and 502 to 514). The lengths are on the
+// device: only their mean is known here.
 int linear_segment(int n_seqs, int64_t total_T, int Hv) {
   const int64_t per_seq = std::max<int64_t>(1, (total_T / std::max(1, n_seqs) + 127) / 128);
   const int64_t blocks = per_seq * n_seqs * Hv;
@@ -389,10 +389,14 @@ int linear_segment(int n_seqs, int64_t total_T, int Hv) {
 // fp32: tokens per segment, and the workspace of the segments' states (what precedes the
 // states holds their decays). Splitting costs a second pass over k and v. Where the
 // sequences' heads fill the GPU by themselves only those of twice the mean length are
-// split (16 x 300 tokens, 32 heads of 128: 425 us, in segments for four waves 692); where a
+// split (16 x 300 tokens, 32 heads of 128: 430 us, in segments for four waves 695); where a
 // wave of resident CTAs holds two segments of each sequence or more, all of them are in one
-// wave (3300 tokens, 16 heads of 64: 85 us, 102 with the last tenth in a second one); in
-// between, in about four.
+// wave (3300 tokens, 16 heads of 64: 96 us, in segments for four waves 119; 4096 tokens, 16
+// heads of 128: 307 and 330); in between, in about four. `resident` is what 148 SMs hold of
+// the kernels' registers and shared memory with two rows a lane; on another device only the
+// choice is off. The rule knows neither how the lengths differ nor what the last wave leaves
+// empty: with 32 heads of 128, 8, 9, 10 and 12 sequences of 2000 tokens take 2.12, 1.53,
+// 2.27 and 2.45 ms, and four of 20 tokens and four of 4000 2.03 ms.
 struct ScanPlan {
   int seg;
   int64_t segments;    // at most

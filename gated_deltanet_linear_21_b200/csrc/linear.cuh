@@ -112,8 +112,9 @@ decode_kernel(const TIO* __restrict__ q, const TIO* __restrict__ k, const TIO* _
 // shared memory, one ahead, where the 8 row groups of a warp read the same q and k words.
 // Those reads are what bounds it, before the arithmetic (three operations a state element
 // and token where o is made, one in the first pass), so a lane holds two rows where d_v
-// has them: one 4096-token sequence of 16 heads of 128 takes 300 us, 32 packed heads of
-// 16 x 300 tokens 425 us; with one row a lane and no stage ahead 477 and 1218.
+// has them: one 4096-token sequence of 16 heads of 128 takes 307 us, 32 packed heads of
+// 16 x 300 tokens 430 us; with one row a lane and no stage ahead 477 and 1218. (Exact decays
+// cost the case of two sequences of 500 to 2000 tokens, 16 heads of 64, 3 us of 88.)
 //
 // Over time. Heads and rows alone give few warps, each with one long chain, so sequences
 // are cut into segments of `seg` tokens, all worked on at once, in three launches: each

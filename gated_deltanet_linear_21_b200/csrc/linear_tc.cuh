@@ -77,17 +77,13 @@
 // that the compute warps wait for none of those; warps 12-15 scan. Sixteen compute warps
 // with half the columns each were slower (560 against 456 us on eight packed sequences).
 //
-// Measured (bf16): 4096 tokens, 16 heads 55 us; eight packed sequences of 128 to 8192 tokens, 32
-// heads 440 us, 780 MB, so 1.8 TB/s; 64 of 20 to 300 tokens 171 us; f16, 32768 tokens, 32
-// heads 471 us. A block takes the compute warps 5200 to 5900 cycles in pass B and 4000 to 5000 in
-// pass A, its products 2560 and 2048: what bounds it is their instructions and waits. Neither
-// fewer spilled registers nor tiles brought to L2 ahead change that.
-//
-// Measured (bf16): 4096 tokens, 16 heads 55 us; eight packed sequences of 128 to 8192 tokens, 32
-// heads 440 us, 780 MB, so 1.8 TB/s; 64 of 20 to 300 tokens 171 us; f16, 32768 tokens, 32
-// heads 471 us. A block takes the compute warps 5200 to 5900 cycles in pass B and 4000 to 5000 in
-// pass A, its products 2560 and 2048: what bounds it is their instructions and waits. Neither
-// fewer spilled registers nor tiles brought to L2 ahead change that.
+// Measured (bf16): 4096 tokens, 16 heads 55 to 56 us; eight packed sequences of 128 to 8192
+// tokens, 32 heads 435 to 440 us, 780 MB, so 1.8 TB/s; 64 of 20 to 300 tokens 173 us; f16, 32768
+// tokens, 32 heads 500 us. A block takes the compute warps 5200 to 5900 cycles in pass B and 4000
+// to 5000 in pass A (f16 some 5 % more: its rows' powers of two), its products 2560 and 2048: what
+// bounds it is their instructions and waits. Neither fewer spilled registers nor tiles brought to
+// L2 ahead change that. Steep blocks cost more: 4096 tokens with g = -1 63 us (f16 70).
+// What finds infinities in V costs 1 to 4 %; looking through each block of V ahead, 7 to 14 %.
 //
 // Order and progress. Items are numbered (sequence, panel, segment, head). Every
 // wait on another CTA is for work of a lower number -- B(i) and scan(i) for scans

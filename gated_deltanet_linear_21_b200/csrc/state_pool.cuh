@@ -20,10 +20,6 @@
 // Measured, 32 heads of 128 x 128, fp32 and e4m3: 64 states stored and loaded again 55.3 us
 // (338 MB, 6.1 TB/s); 48 loaded 23.3 us (5.4 TB/s). With 4 accesses in flight 55.9 and 23.2,
 // with 16 57.3 and 23.5.
-//
-// Measured, 32 heads of 128 x 128, fp32 and e4m3: 64 states stored and loaded again 55.3 us
-// (338 MB, 6.1 TB/s); 48 loaded 23.3 us (5.4 TB/s). With 4 accesses in flight 55.9 and 23.2,
-// with 16 57.3 and 23.5.
 #pragma once
 
 #include <cuda_fp8.h>

@@ -308,8 +308,12 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  *
  * Supported: every dtype, dk and dv in {16, 32, 64, 128}; n_seqs and Hv up to
  * 65535. State and sums are fp32. For bf16 and f16 the state that meets q and
- * the decayed scores are rounded to the input type (o holds no more); the state
- * that is carried is not, and repeated calls give the same bits.
+ * the decayed scores are rounded to the input type, each with its own power of
+ * two in f16; with o's own rounding its error is 1.4 times that of o rounded
+ * alone. The state that is carried is not rounded; what is added to it has 24
+ * bits (bf16) or 22 bits below the largest |k| of 128 tokens (f16). For bf16,
+ * sums of |q . k| |v| over 128 tokens stay below 2^66. Repeated calls give the
+ * same bits.
  */
 size_t gdn_linear_prefill_workspace_bytes(int n_seqs, int64_t total_T, int Hv, int dk, int dv, gdn_dtype dtype);
 gdn_status gdn_linear_prefill(const void *q, const void *k, const void *v,
