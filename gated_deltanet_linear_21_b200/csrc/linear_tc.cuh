@@ -30,7 +30,8 @@
 // 24 bits in bf16. f16 needs hi and rn(w2 k + e1), 22 bits; in bf16 the same two (16
 // bits) serve where the state is only read for o, inside a segment that is not a
 // sequence's last. In f16 powers of two keep what is rounded in the type's range: one
-// from the block's largest |k| and w for the terms of K~; 2^-b for the copy of S; and for
+// from the block's largest |w k| for the terms of K~ (where a column's largest is some 2^-11
+// of it or less, or w falls by 2^-18, one for each column, and the terms come from fp32 products); 2^-b for the copy of S; and for
 // each row r, whose P' and q meet v and that copy in one accumulator, 2^-a_r for P' and
 // 2^(b - a_r) for q (rho_r holds 2^a_r). No row's or state's size then bears on another's
 // precision: a row's largest score (or q, if that is larger) is at 2^14, or q keeps its size
@@ -79,10 +80,10 @@
 //
 // Measured (bf16): 4096 tokens, 16 heads 55 to 56 us; eight packed sequences of 128 to 8192
 // tokens, 32 heads 435 to 440 us, 780 MB, so 1.8 TB/s; 64 of 20 to 300 tokens 173 us; f16, 32768
-// tokens, 32 heads 500 us. A block takes the compute warps 5200 to 5900 cycles in pass B and 4000
-// to 5000 in pass A (f16 some 5 % more: its rows' powers of two), its products 2560 and 2048: what
+// tokens, 32 heads 517 to 532 us. A block takes the compute warps 5200 to 5900 cycles in pass B and
+// 4000 to 5000 in pass A (f16 some 8 % more: its powers of two), its products 2560 and 2048: what
 // bounds it is their instructions and waits. Neither fewer spilled registers nor tiles brought to
-// L2 ahead change that. Steep blocks cost more: 4096 tokens with g = -1 63 us (f16 70).
+// L2 ahead change that. Steep blocks cost more: 4096 tokens with g = -1 62 us (f16 78).
 // What finds infinities in V costs 1 to 4 %; looking through each block of V ahead, 7 to 14 %.
 //
 // Order and progress. Items are numbered (sequence, panel, segment, head). Every
@@ -141,7 +142,7 @@ constexpr uint32_t kTabGam = kTab + 768;       // float gam[128], gp[128], gb[12
 constexpr uint32_t kBars = kTabGam + 1536;
 constexpr uint32_t kRing = kBars + 320;        // items
 constexpr uint32_t kMisc = kRing + 192;        // words: see Misc
-constexpr uint32_t kSmem = kMisc + 192;
+constexpr uint32_t kSmem = kMisc + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 constexpr int kRingItems = 4;
 
@@ -162,13 +163,13 @@ struct Misc {
   uint32_t dead;       // a wait ran out
   float gam_l;         // exp(G_L) of the block
   float2 seg_gam;      // exp of the segment's total log-decay, in two parts (pass A's last block)
-  float w_max;         // the largest w of the block
+  float w_max, w_min;  // the largest and the smallest w of the block's tokens (f16)
   uint32_t steep;      // exp(-G) reaches 2^kSteep in the block
   int start_i[4];      // the log-decays (base 2) up to each quarter: whole part
   float start_f[4];    // and the rest
-  float red[2][kComputeWarps];   // reductions over the compute warps (f16)
+  float red[2][2][kComputeWarps];   // reductions over the compute warps (f16)
 };
-static_assert(sizeof(Misc) <= 192, "shared memory budget");
+static_assert(sizeof(Misc) <= 256, "shared memory budget");
 
 // ---- tensor memory columns ----
 // Each of two terms of K~ has 32 columns for either half of the tokens (0-63, 64-127);
@@ -695,7 +696,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             const double before = lane > 0 ? up : 0.0;   // (not incl - c[3], which a NaN or +inf of this lane would be)
             const double start = __shfl_sync(0xffffffffu, before, lane & 24), whole = floor(start);
             seg += sum;
-            float w[4], wm = 0.f;
+            float w[4], wm = 0.f, wl = kInf;
             float4 gam, gb, gp;
             float *const gamx = &gam.x, *const gbx = &gb.x, *const gpx = &gp.x;
             bool flat = true;
@@ -708,11 +709,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
               gpx[x] = (float)(start - G);
               flat = flat && G > -kSteep;
               wm = fmaxf(wm, w[x]);
+              if (4 * lane + x < L) wl = fminf(wl, w[x]);
             }
             uint2 wp[3];
             if constexpr (kF16) {
 #pragma unroll
-              for (int off = 16; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
+              for (int off = 16; off > 0; off >>= 1) {
+                wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
+                wl = fminf(wl, __shfl_xor_sync(0xffffffffu, wl, off));
+              }
             } else {
               float v[4] = {w[0], w[1], w[2], w[3]};
 #pragma unroll
@@ -744,6 +749,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
             }
             if (lane == 0) {
               misc->w_max = wm;
+              misc->w_min = wl;
               misc->steep = steep;
               misc->gam_l = far_hi;
             }
@@ -902,16 +908,28 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
       arrive_warp(&bars[kCBar]);
       wait_next(kCBar);
     };
-    // the largest value over the compute threads (f16)
-    auto reduce_max = [&](float m) {
+    // the largest value over the compute threads (f16); `low`: the smallest over a warp, then the
+    // smallest over the w4 of the larger of their two warps'
+    auto reduce_max = [&](float m, float* low = nullptr) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      float* red = misc->red[rn++ & 1];   // (the one used two reductions ago: a barrier lies between)
-      if (lane == 0) red[warp] = m;
+      for (int off = 16; off > 0; off >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (low) *low = fminf(*low, __shfl_xor_sync(0xffffffffu, *low, off));
+      }
+      float(*red)[kComputeWarps] = misc->red[rn++ & 1];   // (the one used two reductions ago: a barrier lies between)
+      if (lane == 0) {
+        red[0][warp] = m;
+        if (low) red[1][warp] = *low;
+      }
       sync();
-      m = red[0];
+      m = red[0][0];
 #pragma unroll
-      for (int i = 1; i < kComputeWarps; ++i) m = fmaxf(m, red[i]);
+      for (int i = 1; i < kComputeWarps; ++i) m = fmaxf(m, red[0][i]);
+      if (low) {
+        *low = fmaxf(red[1][0], red[1][4]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) *low = fminf(*low, fmaxf(red[1][i], red[1][4 + i]));
+      }
       return m;
     };
     // the rounded copy of S
@@ -935,23 +953,99 @@ prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ C
 #pragma unroll
       for (int i = 0; i < 8; i += 2) ldmatrix_t4(at + 1024 * i, kr + 2 * i);
     };
+    // f16: the two terms of K~ from fp32 products, a power of two for each column; returns that of
+    // column `row`. ex: the exponents of each half column's largest product. (They are written
+    // behind a barrier that all warps reach after they have read those of an earlier block.)
+    auto put_terms_apart = [&](uint32_t kt, uint32_t region) -> int {
+      uint8_t* const ex = reinterpret_cast<uint8_t*>(tab_w + kB) + 32 * w4;
+      const float* const w = tab_w + 64 * wg + 2 * (lane & 3);
+      auto power = [&](int c) { return min(13 - ((int)max(ex[c], ex[kD + c]) - 127), 126); };
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t kr[16];
+        float m[2] = {0.f, 0.f};
+        load_k(kt, half, kr);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 x = Op16<T>::unpack2(kr[i]);
+          m[i & 1] = fmaxf(m[i & 1], fmaxf(fabsf(x.x * w[8 * (i >> 1)]), fabsf(x.y * w[8 * (i >> 1) + 1])));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+          m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+          if ((lane & 3) == 0) ex[kD * wg + 16 * half + 8 * i + (lane >> 2)] = (uint8_t)(exponent_of(m[i]) + 127);
+        }
+      }
+      sync();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t kr[16], lo[16];
+        load_k(kt, half, kr);
+        const float f[2] = {pow2i(power(16 * half + (lane >> 2))), pow2i(power(16 * half + 8 + (lane >> 2)))};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 x = Op16<T>::unpack2(kr[i]);
+          x.x = x.x * w[8 * (i >> 1)] * f[i & 1];
+          x.y = x.y * w[8 * (i >> 1) + 1] * f[i & 1];
+          kr[i] = Op16<T>::pack2(x.x, x.y);
+          const float2 y = Op16<T>::unpack2(kr[i]);
+          lo[i] = Op16<T>::pack2(x.x - y.x, x.y - y.y);
+        }
+        const uint32_t tw = tl + region + (static_cast<uint32_t>(16 * half) << 16);
+        tmem_st_frag(tw, kr);
+        tmem_st_frag(tw + 32, lo);
+      }
+      return power(lane);
+    };
     // Two terms of K~ (part 0: hi and, with four of them, e1; part 1: h2 and t4). Returns the
     // power of two that they were multiplied with (f16).
     auto put_terms = [&](uint32_t kt, bool four, int part, uint32_t region, int bar) -> int {
       uint32_t w1[8], w2[8], w3[8];
       int e = 0;
       if constexpr (kF16) {
-        __half2 m = __half2half2(__ushort_as_half(0));
+        // The columns' largest products, with w below 1 so that none overflows. f16 ends at 2^-24:
+        // with the block's largest product at 2^13 (w below 2^15) a column's has to be at 2^2 or
+        // above, so that hi and its rest have 22 bits beside it and 18 for what is 2^-8 of it,
+        // and w at 2^-7 or above for 18 bits of its own: a decay of some 18 bits in the block.
+        // Beyond either the terms come from fp32 products, 7 % of a long prompt's time if all do
+        // (551 against 517 us, 32768 tokens; with no look 502).
+        const int ew = exponent_of(misc->w_max);
+        const float ws = pow2i(-ew - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 w = *reinterpret_cast<const float2*>(tab_w + 64 * wg + 8 * i + 2 * (lane & 3));
+          w1[i] = Op16<T>::pack2(w.x * ws, w.y * ws);
+        }
+        float top = 0.f, low = 65504.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t kr[16];
+          __half2 m[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
           load_k(kt, half, kr);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&kr[i])));
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t x = Two<T>::mul(w1[i >> 1], kr[i]);
+            m[i & 1] = __hmax2(m[i & 1], __habs2(*reinterpret_cast<const __half2*>(&x)));
+          }
+          __half2 c = __hmax2(__lows2half2(m[0], m[1]), __highs2half2(m[0], m[1]));   // two columns
+          c = __hmax2(c, __shfl_xor_sync(0xffffffffu, c, 1));
+          c = __hmax2(c, __shfl_xor_sync(0xffffffffu, c, 2));
+          const float2 f = __half22float2(c);
+          const int col = 32 * w4 + 16 * half + (lane >> 2);
+          top = fmaxf(top, fmaxf(f.x, f.y));
+          if (kWhole || col < p.dk) low = fminf(low, f.x);
+          if (kWhole || col + 8 < p.dk) low = fminf(low, f.y);
         }
-        const float2 f = __half22float2(m);
-        // |w k| below 2^14 and w below 2^15 (an infinite k leaves the others their size)
-        e = min(13 - exponent_of(fminf(reduce_max(fmaxf(f.x, f.y)), 65504.f) * misc->w_max), 14 - exponent_of(misc->w_max));
+        top = reduce_max(top, &low);
+        e = min(12 - exponent_of(top) - ew, 14 - ew);
+        if (each_time(!(top < kInf) || low * pow2i(e + ew + 1) < 4.f || misc->w_min * pow2i(e) < 0.0078125f)) {
+          e = put_terms_apart(kt, region);
+          tmem_wait_st();
+          tc_fence_before();
+          arrive_warp(&bars[kKt + bar]);
+          return e;
+        }
         const float scale = pow2i(e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

@@ -40,6 +40,21 @@ def test_a_large_token_leaves_the_others_of_its_block_as_they_were(dtype, at, gr
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("g", [-5.0, -0.7, -0.05])
+@pytest.mark.parametrize("dk", [128, 64])
+def test_small_channels_of_k_keep_their_precision_in_the_state(dtype, g, dk):
+    """Channels and tokens of k at powers of two from 2^-12 to 2^6, so that a channel's part of
+    the state may come from products far below the block's largest."""
+    x = draw([128, 300, 1, 140], 2, 2, dk, 64, dtype, seed=88)
+    gen = torch.Generator().manual_seed(89)
+    size = lambda *shape: torch.exp2(torch.randint(-6, 4, shape, generator=gen).float())  # noqa: E731
+    x["k"] = (x["k"].float() * size(569, 1, 1) * size(1, 2, dk)).to(dtype)
+    x["g"] = torch.full((2,), g)
+    check(x, *prefill(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("bits", [1, 18, 45, 100])
 def test_rows_of_every_size_in_a_block(dtype, bits):
     """q and k of each token, and the state, at their own powers of two."""
