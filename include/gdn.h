@@ -310,9 +310,9 @@ gdn_status gdn_decode_bf16_state(const void *q, const void *k, const void *v,
  * 65535. State and sums are fp32. For bf16 and f16 the state that meets q and
  * the decayed scores are rounded to the input type, each with its own power of
  * two in f16; with o's own rounding its error is 1.4 times that of o rounded
- * alone. The state that is carried is not rounded; what is added to it has 24
- * bits (bf16) or 18 to 22 bits (f16: of products v k that are not below 2^-8 of
- * their channel's largest in 128 tokens, and of others as if they were). For bf16,
+ * alone. The state that is carried is not rounded; exp(G) k, which is added to it
+ * v times, has 24 bits (bf16) or 18 to 22 (f16; where it is below 2^-8 of its
+ * channel's largest in 128 tokens, those of that size). For bf16,
  * sums of |q . k| |v| over 128 tokens stay below 2^66. Repeated calls give the
  * same bits.
  */

@@ -55,6 +55,22 @@ def test_small_channels_of_k_keep_their_precision_in_the_state(dtype, g, dk):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_far_tokens_keep_their_precision_in_the_state(dtype, seed):
+    """Decays of e^-5 a token, tokens of k and v at powers of two from 2^-6 to 2^4: an element of
+    the state may come from a token whose weight is 2^-30."""
+    x = draw([300, 1, 128, 44, 20, 130], 2, 6, 128, 128, dtype, "strong", seed=90 + seed)
+    gen = torch.Generator().manual_seed(91 + seed)
+    for n in "kv":
+        x[n] = (x[n].float() * torch.exp2(torch.randint(-6, 5, (623, x[n].shape[1], 1), generator=gen).float())).to(dtype)
+    o, s = prefill(x)
+    _, rs, _, ms = ref.linear_prefill(x["q"], x["k"], x["v"], x["g"], x["state_in"], x["cu"])
+    for n, T in enumerate([300, 1, 128, 44, 20, 130]):      # each sequence within its own bound
+        ref.check_state(s[n], rs[n], ms[n], min(T, 64))     # (what is older than 64 tokens is gone)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("bits", [1, 18, 45, 100])
 def test_rows_of_every_size_in_a_block(dtype, bits):
     """q and k of each token, and the state, at their own powers of two."""
