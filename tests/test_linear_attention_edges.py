@@ -6,6 +6,7 @@ import os
 import re
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -325,6 +326,41 @@ def test_last_segments_that_follow_one_another_on_a_cta(dtype):
         if i % 10 == 0:
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
     gdn.device_error()
+
+
+# ------------------------------------------------------------------- host threads ---
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["linear_prefill", "prefill"])
+def test_a_new_host_thread_calls_first(name):
+    """A thread that has made no CUDA call yet, with every buffer given, so that nothing before the
+    call makes the device's context the thread's."""
+    x = draw([200], 1, 2, 128, 128, BF16, init=False, seed=95)
+    d = {n: t.to(DEV) for n, t in x.items() if t is not None}
+    beta = torch.full((200, 2), 0.5, device=DEV)
+    o, s = torch.empty_like(d["v"]), torch.empty(1, 2, 128, 128, device=DEV)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    args = (d["q"], d["k"], d["v"], d["g"]) + ((beta,) if name == "prefill" else ()) + (None, d["cu"])
+    want = [t.clone() for t in getattr(gdn, name)(*args, o=o, state_out=s, workspace=ws)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def call():
+        try:
+            getattr(gdn, name)(*args, o=o, state_out=s, workspace=ws)
+        except Exception as e:                # noqa: BLE001
+            failed.append(e)
+
+    for _ in range(20):
+        o.zero_()
+        s.zero_()
+        torch.cuda.synchronize()
+        t = threading.Thread(target=call)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not failed, failed
+        assert torch.equal(o, want[0]) and torch.equal(s, want[1])
 
 
 # ------------------------------------------------------- sizes that are refused ---
