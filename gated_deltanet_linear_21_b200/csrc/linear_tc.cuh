@@ -79,8 +79,8 @@
 // with half the columns each were slower (560 against 456 us on eight packed sequences).
 //
 // Measured (bf16): 4096 tokens, 16 heads 55 to 56 us; eight packed sequences of 128 to 8192
-// tokens, 32 heads 435 to 440 us, 780 MB, so 1.8 TB/s; 64 of 20 to 300 tokens 173 us; f16, 32768
-// tokens, 32 heads 517 to 532 us. A block takes the compute warps 5200 to 5900 cycles in pass B and
+// tokens, 32 heads 435 to 448 us, 780 MB, so 1.8 TB/s; 64 of 20 to 300 tokens 175 us; f16, 32768
+// tokens, 32 heads 517 to 544 us. A block takes the compute warps 5200 to 5900 cycles in pass B and
 // 4000 to 5000 in pass A (f16 some 8 % more: its powers of two), its products 2560 and 2048: what
 // bounds it is their instructions and waits. Neither fewer spilled registers nor tiles brought to
 // L2 ahead change that. Steep blocks cost more: 4096 tokens with g = -1 62 us (f16 78).
